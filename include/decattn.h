@@ -84,7 +84,25 @@ typedef enum {
  *                            tolerance: the oracle runs on the rounded q, and P's rounding is
  *                            bounded per row (see the tests). head_dim 128 and G*T <= 16 only
  *                            (DECATTN_ENOTSUP otherwise). */
-typedef enum { DECATTN_KV_BF16 = 0, DECATTN_KV_FP8E4M3 = 1, DECATTN_KV_FP8E4M3_MMA8 = 2 } decattn_kv_dtype;
+typedef enum {
+  DECATTN_KV_BF16 = 0,
+  DECATTN_KV_FP8E4M3 = 1,
+  DECATTN_KV_FP8E4M3_MMA8 = 2,
+  DECATTN_KV_INT4 = 3
+} decattn_kv_dtype;
+
+/* The INT4 cache (DECATTN_KV_INT4), an extension of this library: the pages name BF16 and FP8 caches only.
+ * A row is the head_dim elements of one token of one KV head, of K or of V.
+ *   codes  k_pages, v_pages: uint8 [num_pages][Hkv][P][head_dim / 2]; element 2 i of a row is in the low four
+ *          bits of byte i, element 2 i + 1 in the high four;
+ *   words  kv_words: uint16 [2][num_pages][Hkv][P] (K, then V), one per row: the word with its four low bits
+ *          cleared is the row's scale s as a bf16 bit pattern, its four low bits are the zero point z.
+ * Element i of a row is s (c_i - z). The scale has at most four significant bits, so every element is a
+ * bf16 number exactly. 4 bits an element and 16 a row: 66 bytes where bf16 takes 256 (head_dim 128).
+ * dec_attn_append_rope_int4 writes such a cache, dec_attn_run_int4 and dec_attn_prefill_int4 read it; their
+ * out is bf16 (the cache's own rounding is about 2^-4 of a row's range). The planners, their plan buffers
+ * and dec_attn_workspace_bytes serve it as they serve the other caches; dec_attn_run and the other entry
+ * points that take fp32 scales return DECATTN_ENOTSUP for it. */
 
 /* Host-side handle of a plan. dec_attn_plan fills it; dec_attn_run reads it. The
  * work list itself lives in the caller's device buffer `buf`. */
@@ -435,6 +453,62 @@ DECATTN_API int dec_attn_prefill_fp8(const dec_attn_shape *shape, const void *q,
                                      const int32_t *seq_lens, const int32_t *cu_q_lens, int64_t total_q_rows,
                                      void *workspace, int64_t workspace_bytes, float *out, float *lse,
                                      int32_t *status, void *stream);
+
+/* dec_attn_append_rope for an INT4 cache, quantising the new K/V rows. Each row x of a new token (k: rotated
+ * as dec_attn_append_rope rotates it and rounded to bf16; v as it is) becomes
+ *     lo = min(0, min_i x_i), hi = max(0, max_i x_i);
+ *     s = the smallest number of four significant bits with 15 s >= hi - lo, at least 2^-126;
+ *     z = rint(-lo / s), c_i = clamp(rint(x_i / s) + z, 0, 15)            (rint: ties to even);
+ * s (c_i - z) lies within s / 2 of x_i. Rows do not depend on one another: older rows of a page are never
+ * touched. A row that holds a NaN, an infinity or a magnitude of 2^127 or more is stored as a NaN row (scale
+ * NaN, codes and z 0): the query rows that see it get NaN, as over a bf16 cache, and no others.
+ * Arguments as dec_attn_append_rope, with shape->kv_dtype DECATTN_KV_INT4 and
+ *   cu_q_lens    NULL: every request has shape->q_tokens new tokens, rows [batch * q_tokens], and total_q_rows
+ *                must be batch * q_tokens; else device int32 [batch + 1], non-decreasing from 0: request b's new
+ *                tokens are the packed rows cu_q_lens[b] .. cu_q_lens[b + 1] - 1, its last positions. Rows
+ *                from cu_q_lens[batch] to total_q_rows (a padded batch) are neither read nor written;
+ *                shape->q_tokens is not used then;
+ *   total_q_rows host: rows of q_new, k_new, v_new, q_out and the values;
+ *   k_pages, v_pages, kv_words  the cache, updated in place (kv_words 2-byte aligned, codes any alignment);
+ *   k_values, v_values  optional (both or neither): bf16 [rows][Hkv][head_dim], the new rows as the cache will
+ *                give them back, also of tokens without a slot: for an attention of the same step over the rows
+ *                at hand, or to see the error of the quantisation.
+ * One kernel. Pages of different requests must be distinct. `status` as dec_attn_append_rope; also
+ * DECATTN_EDEVICE for offsets that do not cover a row below cu_q_lens[batch] (that row is skipped). */
+DECATTN_API int dec_attn_append_rope_int4(const dec_attn_shape *shape, const void *q_new, const void *k_new,
+                                          const void *v_new, const int32_t *page_table, const int32_t *seq_lens,
+                                          const int32_t *cu_q_lens, int64_t total_q_rows, float rope_base,
+                                          void *q_out, void *k_pages, void *v_pages, void *kv_words,
+                                          void *k_values, void *v_values, int32_t *status, void *stream);
+
+/* dec_attn_run over an INT4 cache: split + combine for shape->kv_dtype DECATTN_KV_INT4.
+ *   kv_words  device uint16 [2][num_pages][Hkv][P], 16-byte aligned (codes too);
+ *   out       bf16 [B][T][Hq][d], 16-byte aligned, rounded once from fp32; lse fp32 [B][T][Hq].
+ * Other arguments, shapes, errors and stream rules as dec_attn_run; dense and block-sparse plans. The scores
+ * are exact products of q and the cache's values, summed in fp32; a weight times a V scale is rounded to f16
+ * (2^-11 half a step, below bf16's 2^-9) for the second product. Slots behind a request's last key, their
+ * words among them, may hold anything. */
+DECATTN_API int dec_attn_run_int4(const dec_attn_shape *shape, const void *q, const void *k_pages,
+                                  const void *v_pages, const void *kv_words, const int32_t *page_table,
+                                  const int32_t *seq_lens, const dec_attn_plan_t *plan, void *workspace,
+                                  size_t workspace_bytes, void *out, float *lse, void *stream);
+
+/* Workspace bytes of dec_attn_prefill_int4 for this shape (as dec_attn_prefill_fp8_workspace_bytes). */
+DECATTN_API int64_t dec_attn_prefill_int4_workspace_bytes(const dec_attn_shape *shape);
+
+/* Causal prefill over an INT4 cache (shape->kv_dtype DECATTN_KV_INT4, head_dim 128, page_size a multiple of
+ * 16): the pages of the requests are expanded into `workspace` as a bf16 pool (exact) and the bf16 prefill
+ * kernel runs on it. Arguments as dec_attn_prefill_fp8 with kv_words (16-byte aligned, like codes and
+ * workspace) in place of the scales, and
+ *   out  bf16 [rows][Hq][128], 16-byte aligned, rounded once from fp32; lse fp32 [rows][Hq].
+ * Weights are rounded to bf16 for the second product, as dec_attn_prefill rounds them. A row that sees a NaN
+ * row of the cache gets NaN in out and lse; no other row does. Rows from cu_q_lens[batch] to total_q_rows are
+ * left as they were. */
+DECATTN_API int dec_attn_prefill_int4(const dec_attn_shape *shape, const void *q, const void *k_pages,
+                                      const void *v_pages, const void *kv_words, const int32_t *page_table,
+                                      const int32_t *seq_lens, const int32_t *cu_q_lens, int64_t total_q_rows,
+                                      void *workspace, int64_t workspace_bytes, void *out, float *lse,
+                                      int32_t *status, void *stream);
 
 #ifdef __cplusplus
 }

@@ -25,12 +25,13 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdecattn.so")
 
 OK, EINVAL, ENOTSUP, ESMALL, ECUDA, ETIMEOUT, EDEVICE, EALIGN, ECAPACITY = 0, -1, -2, -3, -4, -5, -6, -7, -8
-KV_BF16, KV_FP8E4M3, KV_FP8E4M3_MMA8 = 0, 1, 2
+KV_BF16, KV_FP8E4M3, KV_FP8E4M3_MMA8, KV_INT4 = 0, 1, 2, 3
 API = ("dec_attn_default_bins", "dec_attn_default_tile_len", "dec_attn_plan_bytes", "dec_attn_plan", "dec_attn_plan_export",
        "dec_attn_workspace_bytes", "dec_attn_run", "dec_attn_split", "dec_attn_combine", "dec_attn_run_noalloc",
        "dec_attn_read_status", "dec_attn_status_string", "dec_attn_append_rope", "dec_attn_append_rope_fp8", "dec_attn_prefill",
        "dec_attn_prefill_varlen", "dec_attn_prefill_fp8_workspace_bytes", "dec_attn_prefill_fp8",
        "dec_attn_plan_sparse_bytes",
+       "dec_attn_append_rope_int4", "dec_attn_run_int4", "dec_attn_prefill_int4_workspace_bytes", "dec_attn_prefill_int4",
        "dec_attn_plan_sparse", "dec_attn_last_error", "dec_attn_test_set_waits")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -115,6 +116,15 @@ def load_library(path: str = LIB_PATH):
         lib.dec_attn_prefill_fp8.argtypes = [C.POINTER(ShapeT), vp, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp,
                                              vp]
         lib.dec_attn_prefill_fp8.restype = i32
+        lib.dec_attn_append_rope_int4.argtypes = [C.POINTER(ShapeT), vp, vp, vp, vp, vp, vp, i64, C.c_float, vp, vp, vp,
+                                                  vp, vp, vp, vp, vp]
+        lib.dec_attn_append_rope_int4.restype = i32
+        lib.dec_attn_run_int4.argtypes = [C.POINTER(ShapeT), vp, vp, vp, vp, vp, vp, C.POINTER(PlanT), vp, sz, vp, vp, vp]
+        lib.dec_attn_run_int4.restype = i32
+        lib.dec_attn_prefill_int4_workspace_bytes.argtypes = [C.POINTER(ShapeT)]
+        lib.dec_attn_prefill_int4_workspace_bytes.restype = i64
+        lib.dec_attn_prefill_int4.argtypes = [C.POINTER(ShapeT), vp, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp, vp]
+        lib.dec_attn_prefill_int4.restype = i32
         lib.dec_attn_test_set_waits.argtypes = [C.c_uint64, C.c_int32]
         lib.dec_attn_test_set_waits.restype = i32
         _lib = lib
@@ -447,6 +457,153 @@ def prefill_fp8_workspace_bytes(q_shape, k_pages: torch.Tensor, page_table: torc
     n = int(load_library().dec_attn_prefill_fp8_workspace_bytes(C.byref(shape)))
     if n < 0:
         raise DecAttnError(n, "dec_attn_prefill_fp8_workspace_bytes")
+    return n
+
+
+def _int4_pools(k_pages: torch.Tensor, v_pages: torch.Tensor, kv_words: torch.Tensor, head_dim: int):
+    """(num_pages, Hkv, P) of an INT4 cache, after the checks that only the tensors allow."""
+    num_pages, Hkv, P, half = k_pages.shape
+    if k_pages.dtype != torch.uint8 or v_pages.dtype != torch.uint8:
+        raise TypeError("INT4 pools are uint8, two codes to a byte")
+    if kv_words.dtype not in (torch.int16, torch.uint16):
+        raise TypeError("kv_words are 16-bit words (int16 or uint16)")
+    if 2 * half != head_dim or v_pages.shape != k_pages.shape or kv_words.shape != (2, num_pages, Hkv, P):
+        raise ValueError("an INT4 cache is k_pages / v_pages [num_pages][Hkv][P][d / 2], kv_words [2][num_pages][Hkv][P]")
+    return num_pages, Hkv, P
+
+
+def _int4_step(rows: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch.Tensor | None,
+               others):
+    """(B, T or 0, total rows) of a call over an INT4 cache. ``rows`` is q: [B][T][Hq][d], or packed
+    [total][Hq][d] with cu_q_lens; ``others`` are its remaining tensors (None: not given). Kernels run on the
+    current device, so every tensor has to be there, and contiguous."""
+    if page_table.dim() != 2 or seq_lens.shape != page_table.shape[:1]:
+        raise ValueError("page_table is [B][max_pages_per_seq] and seq_lens [B]")
+    B = page_table.shape[0]
+    if cu_q_lens is None:
+        if rows.dim() != 4 or rows.shape[0] != B:
+            raise ValueError("q is [B][T][Hq][d], or packed [total][Hq][d] with cu_q_lens")
+        T, total = rows.shape[1], B * rows.shape[1]
+    else:
+        if rows.dim() != 3 or cu_q_lens.shape != (B + 1,):
+            raise ValueError("packed q is [total][Hq][d] with cu_q_lens [B + 1]")
+        T, total = 0, rows.shape[0]
+    if rows.dtype != torch.bfloat16:
+        raise TypeError("q must be bf16")
+    if any(t is not None and t.dtype != torch.int32 for t in (page_table, seq_lens, cu_q_lens)):
+        raise TypeError("page_table, seq_lens and cu_q_lens must be int32")
+    dev = torch.cuda.current_device()
+    for t in (rows, page_table, seq_lens, cu_q_lens, *others):
+        if t is not None and not (t.is_cuda and t.device.index == dev and t.is_contiguous()):
+            raise ValueError("every tensor must be contiguous and on the current CUDA device")
+    return B, T, total
+
+
+def _int4_result(name: str, t: torch.Tensor | None, shape, dtype, device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
+    return t
+
+
+def append_rope_int4(q_new: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, page_table: torch.Tensor,
+                     seq_lens: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_words: torch.Tensor, *,
+                     cu_q_lens: torch.Tensor | None = None, rope_base: float = 10000.0,
+                     q_out: torch.Tensor | None = None, k_values: torch.Tensor | None = None,
+                     v_values: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """dec_attn_append_rope_int4: rotary embedding of the new q / k rows and the quantising append of the new
+    K/V rows into an INT4 cache (k_pages / v_pages uint8 [num_pages][Hkv][P][d / 2], kv_words int16
+    [2][num_pages][Hkv][P], all updated in place); returns the rotated q.
+
+    q_new is bf16 [B][T][Hq][d] (cu_q_lens None), or packed [total][Hq][d] with cu_q_lens int32 [B + 1]
+    holding each request's rows; k_new / v_new likewise with Hkv heads. ``k_values`` / ``v_values``:
+    optional bf16 tensors like k_new (both or neither) that receive the new rows as the cache will give them
+    back; ``status``: optional int32 device scalar (DECATTN_EDEVICE)."""
+    lib = load_library()
+    Hq, d = q_new.shape[-2:]
+    num_pages, Hkv, P = _int4_pools(k_pages, v_pages, kv_words, d)
+    B, T, total = _int4_step(q_new, page_table, seq_lens, cu_q_lens,
+                             (k_new, v_new, q_out, k_values, v_values, k_pages, v_pages, kv_words, status))
+    kv_shape = q_new.shape[:-2] + (Hkv, d)
+    for t in (k_new, v_new, k_values, v_values):
+        if t is not None and (t.shape != kv_shape or t.dtype != torch.bfloat16):
+            raise ValueError("k_new, v_new and the values are bf16, q_new's rows with Hkv heads")
+    q_out = _int4_result("q_out", q_out, q_new.shape, torch.bfloat16, q_new.device)
+    shape = ShapeT(B, Hq, Hkv, d, max(T, 1), P, num_pages, page_table.shape[1], KV_INT4, 0.0)
+    rc = lib.dec_attn_append_rope_int4(C.byref(shape), _ptr(q_new), _ptr(k_new), _ptr(v_new), _ptr(page_table),
+                                       _ptr(seq_lens), _ptr(cu_q_lens), total, rope_base, _ptr(q_out),
+                                       _ptr(k_pages), _ptr(v_pages), _ptr(kv_words), _ptr(k_values), _ptr(v_values),
+                                       _ptr(status), _stream_handle(stream))
+    if rc != OK:
+        raise DecAttnError(rc, "dec_attn_append_rope_int4")
+    return q_out
+
+
+def run_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_words: torch.Tensor,
+             page_table: torch.Tensor, seq_lens: torch.Tensor, pl: Plan, *, sm_scale: float = 0.0,
+             workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+             lse: torch.Tensor | None = None, stream=None):
+    """dec_attn_run_int4: split + combine over an INT4 cache; returns (out bf16 [B][T][Hq][d], lse fp32
+    [B][T][Hq]). q: bf16 [B][T][Hq][d]; the cache as append_rope_int4 writes it; page_table, seq_lens, the
+    plan (dense or block-sparse) and the workspace as for ``run``, the workspace of a shape with KV_INT4."""
+    lib = load_library()
+    Hq, d = q.shape[-2:]
+    num_pages, Hkv, P = _int4_pools(k_pages, v_pages, kv_words, d)
+    B, T, _ = _int4_step(q, page_table, seq_lens, None, (k_pages, v_pages, kv_words, workspace, out, lse))
+    shape = ShapeT(B, Hq, Hkv, d, T, P, num_pages, page_table.shape[1], KV_INT4, sm_scale)
+    out = _int4_result("out", out, q.shape, torch.bfloat16, q.device)
+    lse = _int4_result("lse", lse, q.shape[:-1], torch.float32, q.device)
+    if workspace is None:
+        workspace = torch.empty(workspace_bytes(shape, pl), dtype=torch.uint8, device=q.device)
+    rc = lib.dec_attn_run_int4(C.byref(shape), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(kv_words), _ptr(page_table),
+                               _ptr(seq_lens), C.byref(pl.handle), _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse),
+                               _stream_handle(stream))
+    if rc != OK:
+        raise DecAttnError(rc, "dec_attn_run_int4")
+    return out, lse
+
+
+def prefill_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_words: torch.Tensor,
+                 page_table: torch.Tensor, seq_lens: torch.Tensor, *, cu_q_lens: torch.Tensor | None = None,
+                 max_q_rows: int = 0, sm_scale: float = 0.0, workspace: torch.Tensor | None = None,
+                 out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                 status: torch.Tensor | None = None, stream=None):
+    """dec_attn_prefill_int4: causal prefill over an INT4 cache; returns (out bf16, lse fp32) shaped like q's
+    rows. q is bf16 [B][T][Hq][128] (cu_q_lens None) or packed [total][Hq][128] with cu_q_lens int32 [B + 1] and
+    ``max_q_rows`` bounding every request's rows. ``workspace``: uint8 device buffer of at least
+    prefill_int4_workspace_bytes (allocated here if None)."""
+    lib = load_library()
+    Hq, d = q.shape[-2:]
+    num_pages, Hkv, P = _int4_pools(k_pages, v_pages, kv_words, d)
+    B, T, total = _int4_step(q, page_table, seq_lens, cu_q_lens, (k_pages, v_pages, kv_words, workspace, out, lse, status))
+    shape = ShapeT(B, Hq, Hkv, d, T if cu_q_lens is None else int(max_q_rows), P, num_pages, page_table.shape[1],
+                   KV_INT4, sm_scale)
+    out = _int4_result("out", out, q.shape, torch.bfloat16, q.device)
+    lse = _int4_result("lse", lse, q.shape[:-1], torch.float32, q.device)
+    if workspace is None:
+        need = lib.dec_attn_prefill_int4_workspace_bytes(C.byref(shape))
+        if need < 0:
+            raise DecAttnError(need, "dec_attn_prefill_int4_workspace_bytes")
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    rc = lib.dec_attn_prefill_int4(C.byref(shape), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(kv_words),
+                                   _ptr(page_table), _ptr(seq_lens), _ptr(cu_q_lens), total, _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse), _ptr(status),
+                                   _stream_handle(stream))
+    if rc != OK:
+        raise DecAttnError(rc, "dec_attn_prefill_int4")
+    return out, lse
+
+
+def prefill_int4_workspace_bytes(k_pages: torch.Tensor, page_table: torch.Tensor) -> int:
+    """dec_attn_prefill_int4_workspace_bytes for these pools (the workspace does not depend on q)."""
+    num_pages, Hkv, P, half = k_pages.shape
+    shape = ShapeT(page_table.shape[0], Hkv, Hkv, 2 * half, 1, P, num_pages, page_table.shape[1], KV_INT4, 0.0)
+    n = int(load_library().dec_attn_prefill_int4_workspace_bytes(C.byref(shape)))
+    if n < 0:
+        raise DecAttnError(n, "dec_attn_prefill_int4_workspace_bytes")
     return n
 
 

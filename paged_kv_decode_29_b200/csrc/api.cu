@@ -101,6 +101,20 @@ static bool make_kv_map(CUtensorMap* map, const void* base, int kv_dtype, int D,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// K or V codes of an INT4 cache as a 2-D byte tensor: x = head_dim / 2 bytes, y = (page * Hkv + h) * P + slot.
+// A box is box_rows rows, swizzled to match the kernel's ldmatrix reads.
+static bool make_int4_map(CUtensorMap* map, const void* base, int D, int64_t rows, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)D / 2, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)D / 2};
+  cuuint32_t box[2] = {(cuuint32_t)D / 2, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Prefill queries as a 3-D bf16 tensor {head dim, q head, packed row} (q is [rows][Hq][D]); the
 // kernel loads boxes of 64 head dims x 128 rows with 128-byte swizzle, the K-major layout of the
 // MMA's A operand. Rows past the last one read as zeros.
@@ -116,19 +130,20 @@ static bool make_prefill_q_map(CUtensorMap* map, const void* q, int64_t rows, in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Prefill output as a 3-D fp32 tensor {head dim, q head, packed row} (out is [rows][Hq][D]); the
-// kernel stores boxes of 32 rows x 32 head dims with 128-byte swizzle, only boxes whose rows all
-// belong to one request (the ragged last box of a request is written with plain stores).
-static bool make_prefill_out_map(CUtensorMap* map, float* out, int64_t rows, int Hq, int D) {
+// Prefill output as a 3-D fp32 (or bf16) tensor {head dim, q head, packed row} (out is [rows][Hq][D]);
+// the kernel stores boxes of 32 rows x 32 (64) head dims with 128-byte swizzle, only boxes whose rows
+// all belong to one request (the ragged last box of a request is written with plain stores).
+static bool make_prefill_out_map(CUtensorMap* map, void* out, bool bf16, int64_t rows, int Hq, int D) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
+  const int esz = bf16 ? 2 : 4;
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)rows};
-  cuuint64_t strides[2] = {(cuuint64_t)D * 4, (cuuint64_t)Hq * D * 4};
-  cuuint32_t box[3] = {32, 1, 32};
+  cuuint64_t strides[2] = {(cuuint64_t)D * esz, (cuuint64_t)Hq * D * esz};
+  cuuint32_t box[3] = {(cuuint32_t)(128 / esz), 1, 32};
   cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, out, dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct WsLayout {
@@ -170,7 +185,9 @@ static int check_shape(const dec_attn_shape* s, const dec_attn_plan_t* pl) {
   if (s->head_dim != 64 && s->head_dim != 128) return DECATTN_ENOTSUP;
   if (s->page_size % 16 != 0 || s->page_size > 256) return DECATTN_ENOTSUP;
   if (pl->tile_len % s->page_size != 0) return DECATTN_ENOTSUP;
-  if (s->q_tokens > kMaxT || GT > kMaxGT || !split_supported(s->kv_dtype, s->head_dim, (int)GT))
+  if (s->q_tokens > kMaxT || GT > kMaxGT ||
+      !(s->kv_dtype == DECATTN_KV_INT4 ? split_int4_supported(s->head_dim, (int)GT)
+                                       : split_supported(s->kv_dtype, s->head_dim, (int)GT)))
     return DECATTN_ENOTSUP;
   if ((int64_t)s->num_pages * s->n_kv_heads * s->page_size >= (1ll << 31)) return DECATTN_ENOTSUP;
   if ((int64_t)s->batch * s->q_tokens * s->n_q_heads >= (1ll << 31)) return DECATTN_ENOTSUP;
@@ -178,22 +195,24 @@ static int check_shape(const dec_attn_shape* s, const dec_attn_plan_t* pl) {
 }
 
 // Checks the arguments and enqueues the requested stages (kStageSplit, kStageCombine).
+// kv_words non-null: an INT4 cache (out is bf16); every other cache goes by kv_scales and an fp32 out.
 enum { kStageSplit = 1, kStageCombine = 2 };
 
 static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const void* k_pages, const void* v_pages,
-                   const int32_t* page_table, const int32_t* seq_lens, const float* kv_scales,
-                   const dec_attn_plan_t* plan, void* workspace, size_t workspace_bytes, float* out, float* lse,
-                   void* stream) {
+                   const int32_t* page_table, const int32_t* seq_lens, const float* kv_scales, const void* kv_words,
+                   bool int4, const dec_attn_plan_t* plan, void* workspace, size_t workspace_bytes, void* out,
+                   float* lse, void* stream) {
   int rc = check_shape(shape, plan);
   if (rc != DECATTN_OK) return rc;
   const dec_attn_shape& s = *shape;
+  if ((s.kv_dtype == DECATTN_KV_INT4) != int4) return DECATTN_ENOTSUP;
   if (!workspace) return DECATTN_EINVAL;
   if (s.batch == 0) return DECATTN_OK;
   if (!q || !k_pages || !v_pages || !page_table || !seq_lens || !out || !lse) return DECATTN_EINVAL;
-  if (s.kv_dtype != DECATTN_KV_BF16 && !kv_scales) return DECATTN_EINVAL;
+  if (int4 ? !kv_words : s.kv_dtype != DECATTN_KV_BF16 && !kv_scales) return DECATTN_EINVAL;
   if (s.num_pages <= 0 || s.max_pages_per_seq <= 0) return DECATTN_EINVAL;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(workspace) ||
-      !aligned16(plan->buf))
+      !aligned16(plan->buf) || !aligned16(kv_words))
     return DECATTN_EALIGN;
   if (((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(seq_lens) |
         reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(kv_scales)) & 3) != 0)
@@ -201,7 +220,6 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
   const int G = s.n_q_heads / s.n_kv_heads;
   const int GT = G * s.q_tokens;
   const int D = s.head_dim;
-  (void)GT;
   const WsLayout wl = ws_layout(plan->max_units, s);
   if ((int64_t)workspace_bytes < wl.total) return DECATTN_ESMALL;
   if (wl.items >= (1ll << 31)) return DECATTN_ENOTSUP;  // the combine numbers its items in 32 bits
@@ -217,7 +235,9 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
   if (stages & kStageSplit) {
     CUtensorMap tmK, tmV;
     const int64_t rows = (int64_t)s.num_pages * s.n_kv_heads * s.page_size;
-    if (!make_kv_map(&tmK, k_pages, s.kv_dtype, D, rows) || !make_kv_map(&tmV, v_pages, s.kv_dtype, D, rows))
+    const int box_rows = split_int4_box_rows(s.page_size);
+    if (int4 ? !make_int4_map(&tmK, k_pages, D, rows, box_rows) || !make_int4_map(&tmV, v_pages, D, rows, box_rows)
+             : !make_kv_map(&tmK, k_pages, s.kv_dtype, D, rows) || !make_kv_map(&tmV, v_pages, s.kv_dtype, D, rows))
       return cuda_fail("K/V tensor map (cuTensorMapEncodeTiled)");
     const float scale = s.sm_scale > 0.f ? s.sm_scale : 1.0f / sqrtf((float)D);
     SplitParams sp;
@@ -226,7 +246,10 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
     sp.seq_lens = seq_lens;
     sp.kv_scales = kv_scales;
     sp.plan = static_cast<const char*>(plan->buf);
-    sp.out = out;
+    sp.out = int4 ? nullptr : static_cast<float*>(out);
+    sp.out_bf16 = int4 ? static_cast<uint16_t*>(out) : nullptr;
+    sp.kv_words = static_cast<const uint16_t*>(kv_words);
+    sp.box_rows = box_rows;
     sp.lse = lse;
     sp.part_o = part_o;
     sp.part_lse = part_lse;
@@ -237,8 +260,8 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
     sp.tile_len = plan->tile_len; sp.max_units = plan->max_units; sp.sparse = plan->sparse;
     sp.qk_scale_log2 = scale * 1.4426950408889634f;
     test_waits(&sp.wait_ns, &sp.skip_fill);
-    if (const cudaError_t e = launch_split(sp, tmK, tmV, s.kv_dtype, D, st); e != cudaSuccess)
-      return cuda_fail("split kernel launch", e);
+    const cudaError_t e = int4 ? launch_split_int4(sp, tmK, tmV, D, st) : launch_split(sp, tmK, tmV, s.kv_dtype, D, st);
+    if (e != cudaSuccess) return cuda_fail("split kernel launch", e);
   }
   if (stages & kStageCombine) {
     CombineParams cp;
@@ -246,7 +269,8 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
     cp.seq_lens = seq_lens;
     cp.part_o = part_o;
     cp.part_lse = part_lse;
-    cp.out = out;
+    cp.out = int4 ? nullptr : static_cast<float*>(out);
+    cp.out_bf16 = int4 ? static_cast<uint16_t*>(out) : nullptr;
     cp.lse = lse;
     cp.row_cnt = row_cnt;
     cp.chunk_state = reinterpret_cast<float*>(ws + wl.off_chunk);
@@ -258,12 +282,13 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
   return DECATTN_OK;
 }
 
-// Shared by dec_attn_prefill (cu_q null: T rows per request), dec_attn_prefill_varlen and the FP8
-// prefill (on its widened pool). check_only: every check and tensor map, no launch.
+// Shared by dec_attn_prefill (cu_q null: T rows per request), dec_attn_prefill_varlen and the FP8 and
+// INT4 prefills (on their widened pools; bf16_out: the INT4 prefill's output type). check_only: every
+// check and tensor map, no launch.
 static int prefill_enqueue(const dec_attn_shape* shape, const void* q, const void* k_pages, const void* v_pages,
                            const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_q,
-                           int64_t total_rows, float* out, float* lse, int32_t* status, void* stream,
-                           bool check_only = false) {
+                           int64_t total_rows, void* out, float* lse, int32_t* status, void* stream,
+                           bool check_only = false, bool bf16_out = false) {
   if (!shape) return DECATTN_EINVAL;
   const dec_attn_shape& s = *shape;
   if (s.batch < 0 || s.q_tokens <= 0 || s.n_q_heads <= 0 || s.n_kv_heads <= 0 || s.page_size <= 0 ||
@@ -287,7 +312,7 @@ static int prefill_enqueue(const dec_attn_shape* shape, const void* q, const voi
   if (!make_prefill_q_map(&tmQ, q, total_rows, s.n_q_heads, s.head_dim) ||
       !make_kv_map(&tmK, k_pages, s.kv_dtype, s.head_dim, rows) ||
       !make_kv_map(&tmV, v_pages, s.kv_dtype, s.head_dim, rows) ||
-      !make_prefill_out_map(&tmO, out, total_rows, s.n_q_heads, s.head_dim))
+      !make_prefill_out_map(&tmO, out, bf16_out, total_rows, s.n_q_heads, s.head_dim))
     return cuda_fail("prefill tensor maps (cuTensorMapEncodeTiled)");
   const float scale = s.sm_scale > 0.f ? s.sm_scale : 1.0f / sqrtf((float)s.head_dim);
   PrefillParams p;
@@ -295,7 +320,8 @@ static int prefill_enqueue(const dec_attn_shape* shape, const void* q, const voi
   p.page_table = page_table;
   p.seq_lens = seq_lens;
   p.cu_q = cu_q;
-  p.out = out;
+  p.out = bf16_out ? nullptr : static_cast<float*>(out);
+  p.out_bf16 = bf16_out ? static_cast<uint16_t*>(out) : nullptr;
   p.lse = lse;
   p.status = status;
   p.B = s.batch; p.T = s.q_tokens; p.Hq = s.n_q_heads; p.Hkv = s.n_kv_heads; p.G = s.n_q_heads / s.n_kv_heads;
@@ -356,9 +382,76 @@ static int prefill_fp8_enqueue(const dec_attn_shape* shape, const void* q, const
   return prefill_enqueue(&wide, q, ws, ws + off_v, wide_pt, seq_lens, cu_q, total_rows, out, lse, status, stream);
 }
 
+// INT4 prefill: expand the pages each request uses into the workspace (bf16 pool with its own page
+// table), then the bf16 prefill on it. Every check happens before the first launch.
+static int prefill_int4_enqueue(const dec_attn_shape* shape, const void* q, const void* k_pages, const void* v_pages,
+                                const void* kv_words, const int32_t* page_table, const int32_t* seq_lens,
+                                const int32_t* cu_q, int64_t total_rows, void* workspace, int64_t workspace_bytes,
+                                void* out, float* lse, int32_t* status, void* stream) {
+  const dec_attn_shape& s = *shape;
+  if (s.batch < 0 || s.q_tokens <= 0 || s.n_kv_heads <= 0 || s.page_size <= 0 || s.num_pages < 0 ||
+      s.max_pages_per_seq < 0 || total_rows < 0 || workspace_bytes < 0)
+    return DECATTN_EINVAL;
+  if (s.kv_dtype != DECATTN_KV_INT4 || s.head_dim != 128 || s.page_size % 16 != 0) return DECATTN_ENOTSUP;
+  if ((int64_t)s.batch * s.max_pages_per_seq >= (1ll << 31) || s.n_kv_heads > 65535) return DECATTN_ENOTSUP;
+  if (s.batch == 0 || total_rows == 0) return DECATTN_OK;
+  if (!k_pages || !v_pages || !kv_words || !page_table || !seq_lens || !workspace) return DECATTN_EINVAL;
+  if (s.num_pages <= 0 || s.max_pages_per_seq <= 0) return DECATTN_EINVAL;
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(kv_words) || !aligned16(workspace) ||
+      ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(seq_lens)) & 3) != 0)
+    return DECATTN_EALIGN;
+  int64_t off_v = 0, off_pt = 0;
+  const int64_t need =
+      widen_scratch_bytes(s.batch, s.max_pages_per_seq, s.n_kv_heads, s.page_size, s.head_dim, &off_v, &off_pt);
+  if (workspace_bytes < need) return DECATTN_ESMALL;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  dec_attn_shape wide = s;  // the expanded pool: bf16, page i of request b at b * max_pages_per_seq + i
+  wide.kv_dtype = DECATTN_KV_BF16;
+  wide.num_pages = s.batch * s.max_pages_per_seq;
+  const int32_t* wide_pt = reinterpret_cast<const int32_t*>(ws + off_pt);
+  const int rc = prefill_enqueue(&wide, q, ws, ws + off_v, wide_pt, seq_lens, cu_q, total_rows, out, lse, status,
+                                 stream, /*check_only=*/true, /*bf16_out=*/true);
+  if (rc != DECATTN_OK) return rc;
+  WidenInt4Params w;
+  w.k_codes = static_cast<const uint8_t*>(k_pages);
+  w.v_codes = static_cast<const uint8_t*>(v_pages);
+  w.kv_words = static_cast<const uint16_t*>(kv_words);
+  w.page_table = page_table;
+  w.seq_lens = seq_lens;
+  w.k_out = reinterpret_cast<uint16_t*>(ws);
+  w.v_out = reinterpret_cast<uint16_t*>(ws + off_v);
+  w.pt_out = reinterpret_cast<int32_t*>(ws + off_pt);
+  w.status = status;
+  w.B = s.batch; w.Hkv = s.n_kv_heads; w.P = s.page_size;
+  w.num_pages = s.num_pages; w.mpps = s.max_pages_per_seq;
+  const cudaError_t e = launch_widen_int4(w, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("INT4 prefill expansion launch", e);
+  return prefill_enqueue(&wide, q, ws, ws + off_v, wide_pt, seq_lens, cu_q, total_rows, out, lse, status, stream,
+                         /*check_only=*/false, /*bf16_out=*/true);
+}
+
 }  // namespace decattn
 
 using namespace decattn;
+
+extern "C" int64_t dec_attn_prefill_int4_workspace_bytes(const dec_attn_shape* shape) {
+  if (!shape) return DECATTN_EINVAL;
+  const dec_attn_shape& s = *shape;
+  if (s.batch < 0 || s.n_kv_heads <= 0 || s.page_size <= 0 || s.max_pages_per_seq < 0 || s.head_dim <= 0)
+    return DECATTN_EINVAL;
+  return widen_scratch_bytes(s.batch, s.max_pages_per_seq, s.n_kv_heads, s.page_size, s.head_dim, nullptr, nullptr);
+}
+
+extern "C" int dec_attn_prefill_int4(const dec_attn_shape* shape, const void* q, const void* k_pages,
+                                     const void* v_pages, const void* kv_words, const int32_t* page_table,
+                                     const int32_t* seq_lens, const int32_t* cu_q_lens, int64_t total_q_rows,
+                                     void* workspace, int64_t workspace_bytes, void* out, float* lse,
+                                     int32_t* status, void* stream) {
+  if (!shape) return DECATTN_EINVAL;
+  if (!cu_q_lens && total_q_rows != (int64_t)shape->batch * shape->q_tokens) return DECATTN_EINVAL;
+  return prefill_int4_enqueue(shape, q, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, total_q_rows,
+                              workspace, workspace_bytes, out, lse, status, stream);
+}
 
 extern "C" int64_t dec_attn_prefill_fp8_workspace_bytes(const dec_attn_shape* shape) {
   if (!shape) return DECATTN_EINVAL;
@@ -405,7 +498,8 @@ extern "C" int dec_attn_default_tile_len(int batch, int n_kv_heads, int64_t tota
   if (batch <= 0 || n_kv_heads <= 0 || total_kv_tokens < 0 || page_size <= 0 || page_size % 16 != 0 ||
       head_dim <= 0 || rows_per_kv_head <= 0 || n_bins <= 0)
     return DECATTN_EINVAL;
-  const double elem = kv_dtype == DECATTN_KV_BF16 ? 2.0 : 1.0;
+  // bytes per element; INT4: half a byte, and the two-byte word of a row
+  const double elem = kv_dtype == DECATTN_KV_BF16 ? 2.0 : kv_dtype == DECATTN_KV_INT4 ? 0.5 + 2.0 / head_dim : 1.0;
   const double N = (double)n_bins;
   const double W = (double)n_kv_heads * (double)total_kv_tokens;  // token-heads of the step
   const double tile_cost = 8192.0;  // fixed cost of a tile (q, epilogue, pipeline start) in KV-byte terms
@@ -435,24 +529,32 @@ extern "C" int dec_attn_run(const dec_attn_shape* shape, const void* q, const vo
                             const int32_t* page_table, const int32_t* seq_lens, const float* kv_scales,
                             const dec_attn_plan_t* plan, void* workspace, size_t workspace_bytes, float* out,
                             float* lse, void* stream) {
-  return enqueue(kStageSplit | kStageCombine, shape, q, k_pages, v_pages, page_table,
-                          seq_lens, kv_scales, plan, workspace, workspace_bytes, out, lse, stream);
+  return enqueue(kStageSplit | kStageCombine, shape, q, k_pages, v_pages, page_table, seq_lens, kv_scales, nullptr,
+                 false, plan, workspace, workspace_bytes, out, lse, stream);
+}
+
+extern "C" int dec_attn_run_int4(const dec_attn_shape* shape, const void* q, const void* k_pages, const void* v_pages,
+                                 const void* kv_words, const int32_t* page_table, const int32_t* seq_lens,
+                                 const dec_attn_plan_t* plan, void* workspace, size_t workspace_bytes, void* out,
+                                 float* lse, void* stream) {
+  return enqueue(kStageSplit | kStageCombine, shape, q, k_pages, v_pages, page_table, seq_lens, nullptr, kv_words,
+                 true, plan, workspace, workspace_bytes, out, lse, stream);
 }
 
 extern "C" int dec_attn_split(const dec_attn_shape* shape, const void* q, const void* k_pages, const void* v_pages,
                               const int32_t* page_table, const int32_t* seq_lens, const float* kv_scales,
                               const dec_attn_plan_t* plan, void* workspace, size_t workspace_bytes, float* out,
                               float* lse, void* stream) {
-  return enqueue(kStageSplit, shape, q, k_pages, v_pages, page_table, seq_lens, kv_scales, plan,
-                          workspace, workspace_bytes, out, lse, stream);
+  return enqueue(kStageSplit, shape, q, k_pages, v_pages, page_table, seq_lens, kv_scales, nullptr, false, plan,
+                 workspace, workspace_bytes, out, lse, stream);
 }
 
 extern "C" int dec_attn_combine(const dec_attn_shape* shape, const void* q, const void* k_pages, const void* v_pages,
                                 const int32_t* page_table, const int32_t* seq_lens, const float* kv_scales,
                                 const dec_attn_plan_t* plan, void* workspace, size_t workspace_bytes, float* out,
                                 float* lse, void* stream) {
-  return enqueue(kStageCombine, shape, q, k_pages, v_pages, page_table, seq_lens, kv_scales, plan,
-                          workspace, workspace_bytes, out, lse, stream);
+  return enqueue(kStageCombine, shape, q, k_pages, v_pages, page_table, seq_lens, kv_scales, nullptr, false, plan,
+                 workspace, workspace_bytes, out, lse, stream);
 }
 
 extern "C" int dec_attn_read_status(const dec_attn_plan_t* plan, const void* workspace, void* stream) {

@@ -37,24 +37,33 @@ struct CombineVec {
   using T = typename std::conditional<VEC == 4, float4, float2>::type;
 };
 
-template <int D>
-__device__ __forceinline__ void write_row(float* orow, float* lse_out, int lane, float M, float W,
+// BF16: the row is written to p.out_bf16, rounded once, and a NaN weight (a NaN row of an INT4 cache) is
+// passed on; the fp32 output takes such a row for an empty one.
+template <int D, bool BF16>
+__device__ __forceinline__ void write_row(const CombineParams& p, int64_t row, int lane, float M, float W,
                                           const float (&acc)[D / 32]) {
   constexpr int VEC = D / 32;
   using V = typename CombineVec<D>::T;
-  V v;
-  float* f = reinterpret_cast<float*>(&v);
-  const bool empty = M == -INFINITY || !(W > 0.f);
+  float* lse_out = p.lse + row;
+  const bool empty = BF16 ? W == 0.f : (M == -INFINITY || !(W > 0.f));
   const float inv = empty ? 0.f : 1.f / W;
-  #pragma unroll
-  for (int e = 0; e < VEC; ++e) f[e] = acc[e] * inv;
-  reinterpret_cast<V*>(orow)[lane] = v;
+  if (BF16) {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out_bf16 + row * D) + lane * (VEC / 2);
+    #pragma unroll
+    for (int e = 0; e < VEC; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  } else {
+    V v;
+    float* f = reinterpret_cast<float*>(&v);
+    #pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = acc[e] * inv;
+    reinterpret_cast<V*>(p.out + row * D)[lane] = v;
+  }
   if (lane == 0) *lse_out = empty ? -INFINITY : M + logf(W);
 }
 
 // Items are numbered unit by unit: per request (dense plans: every KV head of a request has the
 // same tiles) or per (request, KV head) pair (block-sparse plans); NU units of RPU query rows.
-template <int D, bool SPARSE>
+template <int D, bool SPARSE, bool BF16>
 __global__ void __launch_bounds__(kCombineThreads, kCombineCtasPerSm) combine_kernel(const CombineParams p) {
   constexpr int VEC = D / 32;
   using V = typename CombineVec<D>::T;
@@ -127,12 +136,11 @@ __global__ void __launch_bounds__(kCombineThreads, kCombineCtasPerSm) combine_ke
         nt = L > 0 ? (L + p.tl - 1) / p.tl : 0;  // == S[b + 1] - S[b]
         slot_base = (int64_t)p.Hkv * S[b] + (int64_t)h * nt;
       }
-      float* orow = p.out + row * D;
       float acc[VEC];
       #pragma unroll
       for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
       if (nt == 0) {  // no key at all
-        write_row<D>(orow, p.lse + row, lane, -INFINITY, 0.f, acc);
+        write_row<D, BF16>(p, row, lane, -INFINITY, 0.f, acc);
         continue;
       }
       const int64_t slot0 = slot_base + (int64_t)j * kCombineChunk;
@@ -153,7 +161,8 @@ __global__ void __launch_bounds__(kCombineThreads, kCombineCtasPerSm) combine_ke
       float M = my_lse;
       #pragma unroll
       for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const float my_w = (lane < n && M != -INFINITY) ? expf(my_lse - M) : 0.f;
+      float my_w = (lane < n && M != -INFINITY) ? expf(my_lse - M) : 0.f;
+      if (BF16 && my_lse != my_lse) my_w = my_lse;  // fmaxf leaves NaNs out of M
       float W = my_w;
       #pragma unroll
       for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
@@ -176,7 +185,7 @@ __global__ void __launch_bounds__(kCombineThreads, kCombineCtasPerSm) combine_ke
         }
       }
       if (ncb == 1) {
-        write_row<D>(orow, p.lse + row, lane, M, W, acc);
+        write_row<D, BF16>(p, row, lane, M, W, acc);
         continue;
       }
       // ---- publish this chunk
@@ -223,9 +232,9 @@ __global__ void __launch_bounds__(kCombineThreads, kCombineCtasPerSm) combine_ke
         #pragma unroll
         for (int o = 16; o > 0; o >>= 1) Mg = fmaxf(Mg, __shfl_xor_sync(0xffffffffu, Mg, o));
         const float Mn = fmaxf(Mt, Mg);
-        if (Mn == -INFINITY) continue;  // no visible key in any chunk so far
+        if (Mn == -INFINITY && !(BF16 && __any_sync(0xffffffffu, wc != wc))) continue;  // no visible key in any chunk so far
         const float a = Mt == -INFINITY ? 0.f : expf(Mt - Mn);
-        const float wl = mc == -INFINITY ? 0.f : expf(mc - Mn);
+        const float wl = mc == -INFINITY ? (BF16 && wc != wc ? 1.f : 0.f) : expf(mc - Mn);
         float Wg = wl * wc;
         #pragma unroll
         for (int o = 16; o > 0; o >>= 1) Wg += __shfl_xor_sync(0xffffffffu, Wg, o);
@@ -243,7 +252,7 @@ __global__ void __launch_bounds__(kCombineThreads, kCombineCtasPerSm) combine_ke
         }
         Mt = Mn;
       }
-      write_row<D>(p.out + row * D, p.lse + row, lane, Mt, Wt, acc);
+      write_row<D, BF16>(p, row, lane, Mt, Wt, acc);
       if (lane == 0) p.row_cnt[row] = 0;  // ready for the next combine on this workspace
     }
   }
@@ -254,8 +263,12 @@ cudaError_t launch_combine(const CombineParams& p, int device, cudaStream_t st) 
   int sms = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return cudaErrorUnknown;
   if (p.D != 128 && p.D != 64) return cudaErrorInvalidValue;
-  const void* fn = p.sparse ? (p.D == 128 ? (const void*)combine_kernel<128, true> : (const void*)combine_kernel<64, true>)
-                            : (p.D == 128 ? (const void*)combine_kernel<128, false> : (const void*)combine_kernel<64, false>);
+  auto pick = [&](auto bf16) -> const void* {
+    constexpr bool BF = decltype(bf16)::value;
+    return p.sparse ? (p.D == 128 ? (const void*)combine_kernel<128, true, BF> : (const void*)combine_kernel<64, true, BF>)
+                    : (p.D == 128 ? (const void*)combine_kernel<128, false, BF> : (const void*)combine_kernel<64, false, BF>);
+  };
+  const void* fn = p.out_bf16 ? pick(std::true_type{}) : pick(std::false_type{});
   const int64_t nu = p.sparse ? (int64_t)p.B * p.Hkv : p.B;
   const int smem = nu <= kCombineSmemRequests ? (int)(4 * (2 * (nu + 1) + p.B + 1)) : 0;
   if (!ensure_smem_attr(fn, smem)) return cudaErrorInvalidValue;

@@ -177,6 +177,9 @@ struct SplitParams {
   float qk_scale_log2;      // sm_scale * log2(e)
   uint64_t wait_ns;         // a pipeline wait gives up after this long (kWaitLimitNs unless a test lowers it)
   int32_t skip_fill;        // tests only: CTA 0's producer leaves this ring fill out (-1: none)
+  const uint16_t* kv_words; // INT4 cache: row words [2][num_pages][Hkv][P] (int4.cuh)
+  uint16_t* out_bf16;       // INT4 cache: bf16 [B][T][Hq][D], in place of out
+  int box_rows;             // INT4 cache: keys per TMA box (split_int4_box_rows)
 };
 
 // Arguments of the prefill kernel (prefill.cu). Query rows are packed: request b's Tb rows are
@@ -189,6 +192,7 @@ struct PrefillParams {
   const int32_t* seq_lens;    // [B]
   const int32_t* cu_q;        // [B + 1] row offsets, or null
   float* out;                 // [total_rows][Hq][D]
+  uint16_t* out_bf16;         // bf16 output in place of out (null: fp32)
   float* lse;                 // [total_rows][Hq]
   int32_t* status;            // optional device word
   int B, T, Hq, Hkv, G, P, num_pages, mpps;
@@ -210,6 +214,20 @@ struct WidenParams {
   int32_t* pt_out;            // [B][mpps]: b * mpps + i
   int32_t* status;            // optional device word
   int B, Hkv, P, D, num_pages, mpps;
+};
+
+// INT4 prefill: the pages each request uses, expanded to a bf16 scratch pool (prefill_int4.cu).
+struct WidenInt4Params {
+  const uint8_t* k_codes;     // [num_pages][Hkv][P][D / 2]
+  const uint8_t* v_codes;
+  const uint16_t* kv_words;   // [2][num_pages][Hkv][P]: K, then V
+  const int32_t* page_table;  // [B][mpps]
+  const int32_t* seq_lens;    // [B]
+  uint16_t* k_out;            // bf16 [B * mpps][Hkv][P][D]: page i of request b at b * mpps + i
+  uint16_t* v_out;
+  int32_t* pt_out;            // [B][mpps]: b * mpps + i
+  int32_t* status;            // optional device word
+  int B, Hkv, P, num_pages, mpps;
 };
 
 // Query rows of one KV head that a decode tile computes at once (G * T), and query tokens per
@@ -238,6 +256,7 @@ struct CombineParams {
   float* chunk_state;       // [items][D + 4]: max, weight, -, -, then the weighted sum
   int B, T, Hq, Hkv, G, GT, D, tl;
   int sparse;               // block-sparse plan: chunks are counted per (request, KV head) pair
+  uint16_t* out_bf16;       // INT4 cache: bf16 output in place of out (null: fp32)
 };
 
 __host__ __device__ inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -484,11 +503,16 @@ int split_ctas_per_sm();                                          // split.cu
 bool split_tc_supported(int kv_dtype, int D, int GT);             // split_tc.cu
 cudaError_t launch_split_tc(const SplitParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, int kv_dtype,
                             cudaStream_t st);                     // split_tc.cu
+bool split_int4_supported(int D, int GT);                         // split_int4.cu
+int split_int4_box_rows(int P);                                   // split_int4.cu
+cudaError_t launch_split_int4(const SplitParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, int D,
+                              cudaStream_t st);                   // split_int4.cu
 cudaError_t launch_combine(const CombineParams& p, int device, cudaStream_t st);  // combine.cu
 cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                            const CUtensorMap& tmV, const CUtensorMap& tmO, cudaStream_t st);  // prefill.cu
 // bytes of the widened pool (K, then V at *off_v, then the page table at *off_pt)   prefill_fp8.cu
 int64_t widen_scratch_bytes(int B, int mpps, int Hkv, int P, int D, int64_t* off_v, int64_t* off_pt);
 cudaError_t launch_widen_kv(const WidenParams& p, cudaStream_t st);  // prefill_fp8.cu
+cudaError_t launch_widen_int4(const WidenInt4Params& p, cudaStream_t st);  // prefill_int4.cu
 
 }  // namespace decattn

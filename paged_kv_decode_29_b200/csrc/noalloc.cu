@@ -97,6 +97,7 @@ extern "C" int dec_attn_run_noalloc(const dec_attn_shape* shape, const void* q, 
                                     const void* v_pages, const int32_t* page_table, const int32_t* seq_lens,
                                     const float* kv_scales, const dec_attn_plan_t* plan, float* out, float* lse,
                                     void* stream) {
+  if (shape && shape->kv_dtype == DECATTN_KV_INT4) return DECATTN_ENOTSUP;  // dec_attn_run_int4 only
   const size_t need = dec_attn_workspace_bytes(shape, plan);
   if (need == 0)  // invalid or unsupported arguments: dec_attn_run reports which, before any launch
     return dec_attn_run(shape, q, k_pages, v_pages, page_table, seq_lens, kv_scales, plan, nullptr, 0, out, lse,

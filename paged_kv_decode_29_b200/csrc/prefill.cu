@@ -155,6 +155,9 @@ __device__ __forceinline__ void pf_bulk_wait_read() {
 // Waits until every bulk group of this thread has completed (its global writes performed).
 __device__ __forceinline__ void pf_bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// BF16OUT: out is bf16 (rounded once from fp32), and a row that saw a NaN keeps it in lse; otherwise
+// out is fp32.
+template <bool BF16OUT>
 __global__ void __launch_bounds__(kPfThreads, 1)
 prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO) {
@@ -469,45 +472,86 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
       tc_fence_after();
       const int t0w = t - lane;  // the warp's first row
       const bool whole_box = t0w + 32 <= Tb;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = (BF16OUT ? l != 0.f : l > 0.f) ? 1.f / l : 0.f;
       uint8_t* stage = sm + L::OFF_Q + warp * 8192;
-      #pragma unroll
-      for (int q4 = 0; q4 < kPfD / 32; ++q4) {
-        float o[32];
-        if (nkb > 0) {
-          tmem_ld32(tO + 32 * q4, o);
-        } else {
-          #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.f;
-        }
-        if (!whole_box) {
-          if (t < Tb) {
-            float4* dst = reinterpret_cast<float4*>(p.out + ((int64_t)(qoff + t) * p.Hq + qh) * kPfD + 32 * q4);
-            #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              dst[c] = make_float4(o[4 * c] * inv, o[4 * c + 1] * inv, o[4 * c + 2] * inv, o[4 * c + 3] * inv);
-          }
-          continue;
-        }
-        uint8_t* box = stage + (q4 & 1) * 4096;
-        if (q4 >= 2) {  // the store that read this box two chunks ago
-          if (lane == 0) pf_bulk_wait_read<1>();
-          __syncwarp();
-        }
+      if (BF16OUT) {
+        // two boxes of 32 rows x 64 head dims, one per 4 KB half of the staging area
         #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<float4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-              make_float4(o[4 * c] * inv, o[4 * c + 1] * inv, o[4 * c + 2] * inv, o[4 * c + 3] * inv);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          pf_tma_store_3d(&tmO, box, 32 * q4, qh, qoff + t0w);
-          pf_bulk_commit();
+        for (int q2 = 0; q2 < kPfD / 64; ++q2) {
+          uint32_t w[32];
+          #pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float o[32];
+            if (nkb > 0) {
+              tmem_ld32(tO + 64 * q2 + 32 * hf, o);
+            } else {
+              #pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            }
+            #pragma unroll
+            for (int i = 0; i < 16; ++i) w[16 * hf + i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+          }
+          if (!whole_box) {
+            if (t < Tb) {
+              uint4* dst = reinterpret_cast<uint4*>(p.out_bf16 + ((int64_t)(qoff + t) * p.Hq + qh) * kPfD + 64 * q2);
+              #pragma unroll
+              for (int c = 0; c < 8; ++c) dst[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+            }
+            continue;
+          }
+          uint8_t* box = stage + q2 * 4096;
+          #pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            pf_tma_store_3d(&tmO, box, 64 * q2, qh, qoff + t0w);
+            pf_bulk_commit();
+          }
+        }
+      } else {
+        #pragma unroll
+        for (int q4 = 0; q4 < kPfD / 32; ++q4) {
+          float o[32];
+          if (nkb > 0) {
+            tmem_ld32(tO + 32 * q4, o);
+          } else {
+            #pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          }
+          if (!whole_box) {
+            if (t < Tb) {
+              float4* dst = reinterpret_cast<float4*>(p.out + ((int64_t)(qoff + t) * p.Hq + qh) * kPfD + 32 * q4);
+              #pragma unroll
+              for (int c = 0; c < 8; ++c)
+                dst[c] = make_float4(o[4 * c] * inv, o[4 * c + 1] * inv, o[4 * c + 2] * inv, o[4 * c + 3] * inv);
+            }
+            continue;
+          }
+          uint8_t* box = stage + (q4 & 1) * 4096;
+          if (q4 >= 2) {  // the store that read this box two chunks ago
+            if (lane == 0) pf_bulk_wait_read<1>();
+            __syncwarp();
+          }
+          #pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<float4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                make_float4(o[4 * c] * inv, o[4 * c + 1] * inv, o[4 * c + 2] * inv, o[4 * c + 3] * inv);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            pf_tma_store_3d(&tmO, box, 32 * q4, qh, qoff + t0w);
+            pf_bulk_commit();
+          }
         }
       }
       if (lane == 0) pf_bulk_wait_all();
       __syncwarp();
-      if (t < Tb) p.lse[(int64_t)(qoff + t) * p.Hq + qh] = l > 0.f ? (mref + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+      if (t < Tb)
+        p.lse[(int64_t)(qoff + t) * p.Hq + qh] =
+            (BF16OUT ? l != 0.f : l > 0.f) ? (mref + __log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
   }
 
@@ -521,7 +565,8 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
 cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                            const CUtensorMap& tmV, const CUtensorMap& tmO, cudaStream_t st) {
   const int smem = PfSmem::ALLOC;
-  if (!ensure_smem_attr((const void*)prefill_kernel, smem)) return cudaErrorInvalidValue;
+  const auto fn = p.out_bf16 ? prefill_kernel<true> : prefill_kernel<false>;
+  if (!ensure_smem_attr((const void*)fn, smem)) return cudaErrorInvalidValue;
   if (p.B == 0 || p.T == 0 || p.Hq == 0) return cudaSuccess;
   const int64_t grid = (int64_t)pf_grid(p.B, p.T, p.Hq, p.G);
   if (grid <= 0 || grid > 0x7fffffff) return cudaErrorInvalidValue;
@@ -530,7 +575,7 @@ cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tmQ, const
   cfg.blockDim = dim3(kPfThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  return cudaLaunchKernelEx(&cfg, prefill_kernel, p, tmQ, tmK, tmV, tmO);
+  return cudaLaunchKernelEx(&cfg, fn, p, tmQ, tmK, tmV, tmO);
 }
 
 }  // namespace decattn
