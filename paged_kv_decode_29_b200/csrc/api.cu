@@ -101,20 +101,6 @@ static bool make_kv_map(CUtensorMap* map, const void* base, int kv_dtype, int D,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// K or V codes of an INT4 cache as a 2-D byte tensor: x = head_dim / 2 bytes, y = (page * Hkv + h) * P + slot.
-// A box is box_rows rows, swizzled to match the kernel's ldmatrix reads.
-static bool make_int4_map(CUtensorMap* map, const void* base, int D, int64_t rows, int box_rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)D / 2, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)D / 2};
-  cuuint32_t box[2] = {(cuuint32_t)D / 2, (cuuint32_t)box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Prefill queries as a 3-D bf16 tensor {head dim, q head, packed row} (q is [rows][Hq][D]); the
 // kernel loads boxes of 64 head dims x 128 rows with 128-byte swizzle, the K-major layout of the
 // MMA's A operand. Rows past the last one read as zeros.
@@ -233,11 +219,9 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
   float* part_lse = reinterpret_cast<float*>(ws + wl.off_part_lse);
 
   if (stages & kStageSplit) {
-    CUtensorMap tmK, tmV;
+    CUtensorMap tmK, tmV;  // the INT4 kernel copies without them
     const int64_t rows = (int64_t)s.num_pages * s.n_kv_heads * s.page_size;
-    const int box_rows = split_int4_box_rows(s.page_size);
-    if (int4 ? !make_int4_map(&tmK, k_pages, D, rows, box_rows) || !make_int4_map(&tmV, v_pages, D, rows, box_rows)
-             : !make_kv_map(&tmK, k_pages, s.kv_dtype, D, rows) || !make_kv_map(&tmV, v_pages, s.kv_dtype, D, rows))
+    if (!int4 && (!make_kv_map(&tmK, k_pages, s.kv_dtype, D, rows) || !make_kv_map(&tmV, v_pages, s.kv_dtype, D, rows)))
       return cuda_fail("K/V tensor map (cuTensorMapEncodeTiled)");
     const float scale = s.sm_scale > 0.f ? s.sm_scale : 1.0f / sqrtf((float)D);
     SplitParams sp;
@@ -248,8 +232,9 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
     sp.plan = static_cast<const char*>(plan->buf);
     sp.out = int4 ? nullptr : static_cast<float*>(out);
     sp.out_bf16 = int4 ? static_cast<uint16_t*>(out) : nullptr;
+    sp.k_codes = static_cast<const uint8_t*>(k_pages);
+    sp.v_codes = static_cast<const uint8_t*>(v_pages);
     sp.kv_words = static_cast<const uint16_t*>(kv_words);
-    sp.box_rows = box_rows;
     sp.lse = lse;
     sp.part_o = part_o;
     sp.part_lse = part_lse;
@@ -260,7 +245,7 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
     sp.tile_len = plan->tile_len; sp.max_units = plan->max_units; sp.sparse = plan->sparse;
     sp.qk_scale_log2 = scale * 1.4426950408889634f;
     test_waits(&sp.wait_ns, &sp.skip_fill);
-    const cudaError_t e = int4 ? launch_split_int4(sp, tmK, tmV, D, st) : launch_split(sp, tmK, tmV, s.kv_dtype, D, st);
+    const cudaError_t e = int4 ? launch_split_int4(sp, D, dev, st) : launch_split(sp, tmK, tmV, s.kv_dtype, D, st);
     if (e != cudaSuccess) return cuda_fail("split kernel launch", e);
   }
   if (stages & kStageCombine) {

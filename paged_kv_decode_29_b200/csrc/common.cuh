@@ -177,9 +177,11 @@ struct SplitParams {
   float qk_scale_log2;      // sm_scale * log2(e)
   uint64_t wait_ns;         // a pipeline wait gives up after this long (kWaitLimitNs unless a test lowers it)
   int32_t skip_fill;        // tests only: CTA 0's producer leaves this ring fill out (-1: none)
-  const uint16_t* kv_words; // INT4 cache: row words [2][num_pages][Hkv][P] (int4.cuh)
-  uint16_t* out_bf16;       // INT4 cache: bf16 [B][T][Hq][D], in place of out
-  int box_rows;             // INT4 cache: keys per TMA box (split_int4_box_rows)
+  // INT4 cache (int4.cuh) only:
+  const uint8_t* k_codes;   // [num_pages][Hkv][P][D / 2]
+  const uint8_t* v_codes;
+  const uint16_t* kv_words; // row words [2][num_pages][Hkv][P]
+  uint16_t* out_bf16;       // bf16 [B][T][Hq][D], in place of out
 };
 
 // Arguments of the prefill kernel (prefill.cu). Query rows are packed: request b's Tb rows are
@@ -504,9 +506,7 @@ bool split_tc_supported(int kv_dtype, int D, int GT);             // split_tc.cu
 cudaError_t launch_split_tc(const SplitParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, int kv_dtype,
                             cudaStream_t st);                     // split_tc.cu
 bool split_int4_supported(int D, int GT);                         // split_int4.cu
-int split_int4_box_rows(int P);                                   // split_int4.cu
-cudaError_t launch_split_int4(const SplitParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, int D,
-                              cudaStream_t st);                   // split_int4.cu
+cudaError_t launch_split_int4(const SplitParams& p, int D, int device, cudaStream_t st);  // split_int4.cu
 cudaError_t launch_combine(const CombineParams& p, int device, cudaStream_t st);  // combine.cu
 cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                            const CUtensorMap& tmV, const CUtensorMap& tmO, cudaStream_t st);  // prefill.cu

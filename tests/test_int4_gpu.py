@@ -374,16 +374,13 @@ def test_decode_is_the_same_twice_on_a_stream_and_in_a_graph():
     assert np.array_equal(_f64(bufs[1][1]), ref2[0]) and np.array_equal(_f64(bufs[1][2]), ref2[1])
 
 
-@pytest.mark.parametrize("hq,T,d", [(8, 1, 128), (16, 2, 128), (16, 4, 64), (64, 1, 128)])
-def test_decode_wait_runs_out_then_the_context_is_usable(hq, T, d):
-    cache = I4.Cache([3000, 2500, 4000], Hkv=1 if hq == 64 else 2, d=d, P=16, seed=31)
-    q = I4.bf16(np.random.default_rng(32).standard_normal((3, T, hq, d)))
-    try:
-        da.test_set_waits(1_000_000, 2)
-        _decode(cache, q, T, tile=512, expect=da.ETIMEOUT)
-    finally:
-        da.test_set_waits(0, -1)
-    out, lse = _decode(cache, q, T, tile=512)
+@pytest.mark.parametrize("n_bins", [1, 2, 5])
+@pytest.mark.parametrize("hq,T", [(8, 1), (16, 2), (24, 2), (48, 2)])
+def test_decode_of_many_short_tiles_in_few_bins(hq, T, n_bins):
+    """A CTA walks hundreds of tiles of one block, more than it fetches descriptors for at a time."""
+    cache = I4.Cache([16 * 70, 0, 5, 16 * 33 + 1], Hkv=2, d=128, P=16, seed=33)
+    q = I4.bf16(np.random.default_rng(34).standard_normal((4, T, hq, 128)))
+    out, lse = _decode(cache, q, T, tile=16, n_bins=n_bins)
     _check_decode(cache, q, T, out, lse)
 
 
