@@ -469,7 +469,8 @@ DECATTN_API int dec_attn_prefill_fp8(const dec_attn_shape *shape, const void *q,
  *                from cu_q_lens[batch] to total_q_rows (a padded batch) are neither read nor written;
  *                shape->q_tokens is not used then;
  *   total_q_rows host: rows of q_new, k_new, v_new, q_out and the values;
- *   k_pages, v_pages, kv_words  the cache, updated in place (kv_words 2-byte aligned, codes any alignment);
+ *   k_pages, v_pages, kv_words  the cache, updated in place (kv_words 2-byte aligned; codes, like the rows and
+ *                q_out, 16-byte aligned);
  *   k_values, v_values  optional (both or neither): bf16 [rows][Hkv][head_dim], the new rows as the cache will
  *                give them back, also of tokens without a slot: for an attention of the same step over the rows
  *                at hand, or to see the error of the quantisation.

@@ -147,8 +147,8 @@ def last_error() -> str:
 
 
 def _stream_handle(stream) -> int | None:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the raw handle: a torch.cuda.Stream object would take 3 us to make
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
     h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     return h or None
 
@@ -460,49 +460,48 @@ def prefill_fp8_workspace_bytes(q_shape, k_pages: torch.Tensor, page_table: torc
     return n
 
 
-def _int4_pools(k_pages: torch.Tensor, v_pages: torch.Tensor, kv_words: torch.Tensor, head_dim: int):
-    """(num_pages, Hkv, P) of an INT4 cache, after the checks that only the tensors allow."""
-    num_pages, Hkv, P, half = k_pages.shape
-    if k_pages.dtype != torch.uint8 or v_pages.dtype != torch.uint8:
-        raise TypeError("INT4 pools are uint8, two codes to a byte")
-    if kv_words.dtype not in (torch.int16, torch.uint16):
-        raise TypeError("kv_words are 16-bit words (int16 or uint16)")
-    if 2 * half != head_dim or v_pages.shape != k_pages.shape or kv_words.shape != (2, num_pages, Hkv, P):
-        raise ValueError("an INT4 cache is k_pages / v_pages [num_pages][Hkv][P][d / 2], kv_words [2][num_pages][Hkv][P]")
-    return num_pages, Hkv, P
-
-
-def _int4_step(rows: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch.Tensor | None,
-               others):
-    """(B, T or 0, total rows) of a call over an INT4 cache. ``rows`` is q: [B][T][Hq][d], or packed
-    [total][Hq][d] with cu_q_lens; ``others`` are its remaining tensors (None: not given). Kernels run on the
-    current device, so every tensor has to be there, and contiguous."""
-    if page_table.dim() != 2 or seq_lens.shape != page_table.shape[:1]:
-        raise ValueError("page_table is [B][max_pages_per_seq] and seq_lens [B]")
-    B = page_table.shape[0]
+def _int4_args(rows: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_words: torch.Tensor,
+               page_table: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch.Tensor | None, *others):
+    """The shape of a call over an INT4 cache and its total rows, after the checks that only the tensors allow.
+    ``rows`` is q: [B][T][Hq][d], or packed [total][Hq][d] with cu_q_lens (q_tokens is 1 then); ``others`` are its
+    remaining tensors (None: not given). Kernels run on the current device, so every tensor has to be there."""
+    q_shape, pool_shape = rows.shape, k_pages.shape
+    B, mpps = page_table.shape
     if cu_q_lens is None:
-        if rows.dim() != 4 or rows.shape[0] != B:
+        if len(q_shape) != 4 or q_shape[0] != B:
             raise ValueError("q is [B][T][Hq][d], or packed [total][Hq][d] with cu_q_lens")
-        T, total = rows.shape[1], B * rows.shape[1]
+        T = q_shape[1]
+        total = B * T
     else:
-        if rows.dim() != 3 or cu_q_lens.shape != (B + 1,):
+        if len(q_shape) != 3 or cu_q_lens.shape != (B + 1,):
             raise ValueError("packed q is [total][Hq][d] with cu_q_lens [B + 1]")
-        T, total = 0, rows.shape[0]
+        if cu_q_lens.dtype != torch.int32:
+            raise TypeError("cu_q_lens must be int32")
+        T, total = 1, q_shape[0]
+    if seq_lens.shape != (B,):
+        raise ValueError("page_table is [B][max_pages_per_seq] and seq_lens [B]")
     if rows.dtype != torch.bfloat16:
         raise TypeError("q must be bf16")
-    if any(t is not None and t.dtype != torch.int32 for t in (page_table, seq_lens, cu_q_lens)):
-        raise TypeError("page_table, seq_lens and cu_q_lens must be int32")
+    if page_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        raise TypeError("page_table and seq_lens must be int32")
+    if k_pages.dtype != torch.uint8 or v_pages.dtype != torch.uint8:
+        raise TypeError("INT4 pools are uint8, two codes to a byte")
+    if kv_words.dtype != torch.int16 and kv_words.dtype != torch.uint16:
+        raise TypeError("kv_words are 16-bit words (int16 or uint16)")
+    if (len(pool_shape) != 4 or 2 * pool_shape[3] != q_shape[-1] or v_pages.shape != pool_shape
+            or kv_words.shape != (2,) + pool_shape[:3]):
+        raise ValueError("an INT4 cache is k_pages / v_pages [num_pages][Hkv][P][d / 2], kv_words [2][num_pages][Hkv][P]")
     dev = torch.cuda.current_device()
-    for t in (rows, page_table, seq_lens, cu_q_lens, *others):
-        if t is not None and not (t.is_cuda and t.device.index == dev and t.is_contiguous()):
+    for t in (rows, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, *others):
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
             raise ValueError("every tensor must be contiguous and on the current CUDA device")
-    return B, T, total
+    return ShapeT(B, q_shape[-2], pool_shape[1], q_shape[-1], T, pool_shape[2], pool_shape[0], mpps, KV_INT4, 0.0), total
 
 
-def _int4_result(name: str, t: torch.Tensor | None, shape, dtype, device) -> torch.Tensor:
+def _int4_result(name: str, t: torch.Tensor | None, shape, dtype, like: torch.Tensor) -> torch.Tensor:
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.shape != shape or t.dtype != dtype:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
     return t
 
@@ -522,16 +521,13 @@ def append_rope_int4(q_new: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
     optional bf16 tensors like k_new (both or neither) that receive the new rows as the cache will give them
     back; ``status``: optional int32 device scalar (DECATTN_EDEVICE)."""
     lib = load_library()
-    Hq, d = q_new.shape[-2:]
-    num_pages, Hkv, P = _int4_pools(k_pages, v_pages, kv_words, d)
-    B, T, total = _int4_step(q_new, page_table, seq_lens, cu_q_lens,
-                             (k_new, v_new, q_out, k_values, v_values, k_pages, v_pages, kv_words, status))
-    kv_shape = q_new.shape[:-2] + (Hkv, d)
+    shape, total = _int4_args(q_new, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, k_new, v_new, q_out,
+                              k_values, v_values, status)
+    kv_shape = (*q_new.shape[:-2], shape.n_kv_heads, shape.head_dim)
     for t in (k_new, v_new, k_values, v_values):
         if t is not None and (t.shape != kv_shape or t.dtype != torch.bfloat16):
             raise ValueError("k_new, v_new and the values are bf16, q_new's rows with Hkv heads")
-    q_out = _int4_result("q_out", q_out, q_new.shape, torch.bfloat16, q_new.device)
-    shape = ShapeT(B, Hq, Hkv, d, max(T, 1), P, num_pages, page_table.shape[1], KV_INT4, 0.0)
+    q_out = _int4_result("q_out", q_out, q_new.shape, torch.bfloat16, q_new)
     rc = lib.dec_attn_append_rope_int4(C.byref(shape), _ptr(q_new), _ptr(k_new), _ptr(v_new), _ptr(page_table),
                                        _ptr(seq_lens), _ptr(cu_q_lens), total, rope_base, _ptr(q_out),
                                        _ptr(k_pages), _ptr(v_pages), _ptr(kv_words), _ptr(k_values), _ptr(v_values),
@@ -549,12 +545,10 @@ def run_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_w
     [B][T][Hq]). q: bf16 [B][T][Hq][d]; the cache as append_rope_int4 writes it; page_table, seq_lens, the
     plan (dense or block-sparse) and the workspace as for ``run``, the workspace of a shape with KV_INT4."""
     lib = load_library()
-    Hq, d = q.shape[-2:]
-    num_pages, Hkv, P = _int4_pools(k_pages, v_pages, kv_words, d)
-    B, T, _ = _int4_step(q, page_table, seq_lens, None, (k_pages, v_pages, kv_words, workspace, out, lse))
-    shape = ShapeT(B, Hq, Hkv, d, T, P, num_pages, page_table.shape[1], KV_INT4, sm_scale)
-    out = _int4_result("out", out, q.shape, torch.bfloat16, q.device)
-    lse = _int4_result("lse", lse, q.shape[:-1], torch.float32, q.device)
+    shape, _ = _int4_args(q, k_pages, v_pages, kv_words, page_table, seq_lens, None, workspace, out, lse)
+    shape.sm_scale = sm_scale
+    out = _int4_result("out", out, q.shape, torch.bfloat16, q)
+    lse = _int4_result("lse", lse, q.shape[:-1], torch.float32, q)
     if workspace is None:
         workspace = torch.empty(workspace_bytes(shape, pl), dtype=torch.uint8, device=q.device)
     rc = lib.dec_attn_run_int4(C.byref(shape), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(kv_words), _ptr(page_table),
@@ -576,13 +570,12 @@ def prefill_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     ``max_q_rows`` bounding every request's rows. ``workspace``: uint8 device buffer of at least
     prefill_int4_workspace_bytes (allocated here if None)."""
     lib = load_library()
-    Hq, d = q.shape[-2:]
-    num_pages, Hkv, P = _int4_pools(k_pages, v_pages, kv_words, d)
-    B, T, total = _int4_step(q, page_table, seq_lens, cu_q_lens, (k_pages, v_pages, kv_words, workspace, out, lse, status))
-    shape = ShapeT(B, Hq, Hkv, d, T if cu_q_lens is None else int(max_q_rows), P, num_pages, page_table.shape[1],
-                   KV_INT4, sm_scale)
-    out = _int4_result("out", out, q.shape, torch.bfloat16, q.device)
-    lse = _int4_result("lse", lse, q.shape[:-1], torch.float32, q.device)
+    shape, total = _int4_args(q, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, workspace, out, lse, status)
+    shape.sm_scale = sm_scale
+    if cu_q_lens is not None:
+        shape.q_tokens = int(max_q_rows)
+    out = _int4_result("out", out, q.shape, torch.bfloat16, q)
+    lse = _int4_result("lse", lse, q.shape[:-1], torch.float32, q)
     if workspace is None:
         need = lib.dec_attn_prefill_int4_workspace_bytes(C.byref(shape))
         if need < 0:

@@ -103,10 +103,10 @@ def test_append_rejects_bad_args(lib):
         assert _append(lib, s, **{name: None}) == da.EINVAL
     assert _append(lib, s, kv=FAKE) == da.EINVAL                     # both values or neither
     assert _append(lib, s, vv=FAKE) == da.EINVAL
-    for name in ("qn", "kn", "vn", "qo"):
-        assert _append(lib, s, **{name: FAKE + 2}) == da.EALIGN      # d = 128: 4-byte accesses
-        assert _append(lib, _shape(head_dim=64), **{name: FAKE + 1}) == da.EALIGN
-    assert _append(lib, s, kv=FAKE + 2, vv=FAKE) == da.EALIGN
+    for name in ("qn", "kn", "vn", "qo", "kp", "vp"):
+        assert _append(lib, s, **{name: FAKE + 8}) == da.EALIGN
+        assert _append(lib, _shape(head_dim=64), **{name: FAKE + 4}) == da.EALIGN
+    assert _append(lib, s, kv=FAKE + 8, vv=FAKE) == da.EALIGN
     assert _append(lib, s, w=FAKE + 1) == da.EALIGN
     for name in ("tab", "lens", "cu", "st"):
         assert _append(lib, s, **{name: FAKE + 2}) == da.EALIGN
