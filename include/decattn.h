@@ -494,15 +494,18 @@ DECATTN_API int dec_attn_run_int4(const dec_attn_shape *shape, const void *q, co
                                   const int32_t *seq_lens, const dec_attn_plan_t *plan, void *workspace,
                                   size_t workspace_bytes, void *out, float *lse, void *stream);
 
-/* Workspace bytes of dec_attn_prefill_int4 for this shape (as dec_attn_prefill_fp8_workspace_bytes). */
+/* Workspace bytes of dec_attn_prefill_int4 for this shape (batch, q_tokens, heads and pages count), negative on an
+ * error. */
 DECATTN_API int64_t dec_attn_prefill_int4_workspace_bytes(const dec_attn_shape *shape);
 
 /* Causal prefill over an INT4 cache (shape->kv_dtype DECATTN_KV_INT4, head_dim 128, page_size a multiple of
  * 16): the pages of the requests are expanded into `workspace` as a bf16 pool (exact) and the bf16 prefill
  * kernel runs on it. Arguments as dec_attn_prefill_fp8 with kv_words (16-byte aligned, like codes and
  * workspace) in place of the scales, and
+ *   total_q_rows  at most batch * q_tokens (DECATTN_EINVAL otherwise): q_tokens bounds every request's rows;
  *   out  bf16 [rows][Hq][128], 16-byte aligned, rounded once from fp32; lse fp32 [rows][Hq].
- * Weights are rounded to bf16 for the second product, as dec_attn_prefill rounds them. A row that sees a NaN
+ * Where the rows are few, the keys of a request are split over several CTAs and their fp32 parts merged (third
+ * launch). Weights are rounded to bf16 for the second product, as dec_attn_prefill rounds them. A row that sees a NaN
  * row of the cache gets NaN in out and lse; no other row does. Rows from cu_q_lens[batch] to total_q_rows are
  * left as they were. */
 DECATTN_API int dec_attn_prefill_int4(const dec_attn_shape *shape, const void *q, const void *k_pages,

@@ -590,10 +590,12 @@ def prefill_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     return out, lse
 
 
-def prefill_int4_workspace_bytes(k_pages: torch.Tensor, page_table: torch.Tensor) -> int:
-    """dec_attn_prefill_int4_workspace_bytes for these pools (the workspace does not depend on q)."""
+def prefill_int4_workspace_bytes(q_shape, k_pages: torch.Tensor, page_table: torch.Tensor, max_q_rows: int = 0) -> int:
+    """dec_attn_prefill_int4_workspace_bytes for q of this shape ([B][T][Hq][128], or packed [total][Hq][128] with
+    ``max_q_rows``) and these pools."""
     num_pages, Hkv, P, half = k_pages.shape
-    shape = ShapeT(page_table.shape[0], Hkv, Hkv, 2 * half, 1, P, num_pages, page_table.shape[1], KV_INT4, 0.0)
+    T = int(q_shape[1]) if len(q_shape) == 4 else int(max_q_rows)
+    shape = ShapeT(page_table.shape[0], int(q_shape[-2]), Hkv, 2 * half, T, P, num_pages, page_table.shape[1], KV_INT4, 0.0)
     n = int(load_library().dec_attn_prefill_int4_workspace_bytes(C.byref(shape)))
     if n < 0:
         raise DecAttnError(n, "dec_attn_prefill_int4_workspace_bytes")

@@ -268,12 +268,13 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
 }
 
 // Shared by dec_attn_prefill (cu_q null: T rows per request), dec_attn_prefill_varlen and the FP8 and
-// INT4 prefills (on their widened pools; bf16_out: the INT4 prefill's output type). check_only: every
-// check and tensor map, no launch.
+// INT4 prefills (on their widened pools; splits > 0: the INT4 prefill's, with a bf16 output and room for the
+// parts of so many splits). check_only: every check and tensor map, no launch.
 static int prefill_enqueue(const dec_attn_shape* shape, const void* q, const void* k_pages, const void* v_pages,
                            const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_q,
                            int64_t total_rows, void* out, float* lse, int32_t* status, void* stream,
-                           bool check_only = false, bool bf16_out = false) {
+                           bool check_only = false, int splits = 0, float* parts = nullptr) {
+  const bool bf16_out = splits > 0;
   if (!shape) return DECATTN_EINVAL;
   const dec_attn_shape& s = *shape;
   if (s.batch < 0 || s.q_tokens <= 0 || s.n_q_heads <= 0 || s.n_kv_heads <= 0 || s.page_size <= 0 ||
@@ -292,13 +293,15 @@ static int prefill_enqueue(const dec_attn_shape* shape, const void* q, const voi
         reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(status) | reinterpret_cast<uintptr_t>(cu_q)) &
        3) != 0)
     return DECATTN_EALIGN;
-  CUtensorMap tmQ, tmK, tmV, tmO;
+  CUtensorMap tmQ, tmK, tmV, tmO, tmP;
   const int64_t rows = (int64_t)s.num_pages * s.n_kv_heads * s.page_size;
   if (!make_prefill_q_map(&tmQ, q, total_rows, s.n_q_heads, s.head_dim) ||
       !make_kv_map(&tmK, k_pages, s.kv_dtype, s.head_dim, rows) ||
       !make_kv_map(&tmV, v_pages, s.kv_dtype, s.head_dim, rows) ||
-      !make_prefill_out_map(&tmO, out, bf16_out, total_rows, s.n_q_heads, s.head_dim))
+      !make_prefill_out_map(&tmO, out, bf16_out, total_rows, s.n_q_heads, s.head_dim) ||
+      (splits > 1 && !make_prefill_out_map(&tmP, parts, false, splits * total_rows, s.n_q_heads, s.head_dim)))
     return cuda_fail("prefill tensor maps (cuTensorMapEncodeTiled)");
+  if (splits <= 1) tmP = tmO;  // not used
   const float scale = s.sm_scale > 0.f ? s.sm_scale : 1.0f / sqrtf((float)s.head_dim);
   PrefillParams p;
   p.q = static_cast<const uint16_t*>(q);
@@ -312,10 +315,13 @@ static int prefill_enqueue(const dec_attn_shape* shape, const void* q, const voi
   p.B = s.batch; p.T = s.q_tokens; p.Hq = s.n_q_heads; p.Hkv = s.n_kv_heads; p.G = s.n_q_heads / s.n_kv_heads;
   p.P = s.page_size; p.num_pages = s.num_pages; p.mpps = s.max_pages_per_seq;
   p.total_rows = total_rows;
+  p.splits = splits > 0 ? splits : 1;
+  p.part_o = parts;
+  p.part_lse = parts ? parts + p.splits * total_rows * s.n_q_heads * s.head_dim : nullptr;
   p.qk_scale_log2 = scale * 1.4426950408889634f;
   test_waits(&p.wait_ns, &p.skip_fill);
   if (check_only) return DECATTN_OK;
-  const cudaError_t e = launch_prefill(p, tmQ, tmK, tmV, tmO, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_prefill(p, tmQ, tmK, tmV, tmO, tmP, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DECATTN_OK : cuda_fail("prefill kernel launch", e);
 }
 
@@ -367,6 +373,18 @@ static int prefill_fp8_enqueue(const dec_attn_shape* shape, const void* q, const
   return prefill_enqueue(&wide, q, ws, ws + off_v, wide_pt, seq_lens, cu_q, total_rows, out, lse, status, stream);
 }
 
+// Workspace of the INT4 prefill: the expanded pools and their page table (widen_scratch_bytes), then, where the
+// keys are split, the parts of batch * q_tokens rows (fp32 out and lse).
+static int64_t prefill_int4_scratch(const dec_attn_shape& s, int64_t* off_v, int64_t* off_pt, int64_t* off_parts, int* splits) {
+  const int64_t wide =
+      widen_scratch_bytes(s.batch, s.max_pages_per_seq, s.n_kv_heads, s.page_size, s.head_dim, off_v, off_pt);
+  const int64_t rows = (int64_t)s.batch * s.q_tokens;
+  const int n = rows > 0 ? prefill_splits(s.batch, s.q_tokens, s.n_q_heads, s.n_q_heads / s.n_kv_heads) : 1;
+  if (off_parts) *off_parts = wide;
+  if (splits) *splits = n;
+  return wide + (n > 1 ? align_up(n * rows * s.n_q_heads * (s.head_dim + 1) * 4, 256) : 0);
+}
+
 // INT4 prefill: expand the pages each request uses into the workspace (bf16 pool with its own page
 // table), then the bf16 prefill on it. Every check happens before the first launch.
 static int prefill_int4_enqueue(const dec_attn_shape* shape, const void* q, const void* k_pages, const void* v_pages,
@@ -377,7 +395,11 @@ static int prefill_int4_enqueue(const dec_attn_shape* shape, const void* q, cons
   if (s.batch < 0 || s.q_tokens <= 0 || s.n_kv_heads <= 0 || s.page_size <= 0 || s.num_pages < 0 ||
       s.max_pages_per_seq < 0 || total_rows < 0 || workspace_bytes < 0)
     return DECATTN_EINVAL;
+  if (s.n_q_heads <= 0 || s.n_q_heads % s.n_kv_heads != 0) return DECATTN_EINVAL;
   if (s.kv_dtype != DECATTN_KV_INT4 || s.head_dim != 128 || s.page_size % 16 != 0) return DECATTN_ENOTSUP;
+  if (s.batch > 65535 || s.n_q_heads > 65535 || (int64_t)s.batch * s.q_tokens * s.n_q_heads >= (1ll << 31))
+    return DECATTN_ENOTSUP;
+  if (total_rows > (int64_t)s.batch * s.q_tokens) return DECATTN_EINVAL;  // q_tokens bounds every request's rows
   if ((int64_t)s.batch * s.max_pages_per_seq >= (1ll << 31) || s.n_kv_heads > 65535) return DECATTN_ENOTSUP;
   if (s.batch == 0 || total_rows == 0) return DECATTN_OK;
   if (!k_pages || !v_pages || !kv_words || !page_table || !seq_lens || !workspace) return DECATTN_EINVAL;
@@ -385,17 +407,18 @@ static int prefill_int4_enqueue(const dec_attn_shape* shape, const void* q, cons
   if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(kv_words) || !aligned16(workspace) ||
       ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(seq_lens)) & 3) != 0)
     return DECATTN_EALIGN;
-  int64_t off_v = 0, off_pt = 0;
-  const int64_t need =
-      widen_scratch_bytes(s.batch, s.max_pages_per_seq, s.n_kv_heads, s.page_size, s.head_dim, &off_v, &off_pt);
+  int64_t off_v = 0, off_pt = 0, off_parts = 0;
+  int splits = 1;
+  const int64_t need = prefill_int4_scratch(s, &off_v, &off_pt, &off_parts, &splits);
   if (workspace_bytes < need) return DECATTN_ESMALL;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* parts = splits > 1 ? reinterpret_cast<float*>(ws + off_parts) : nullptr;
   dec_attn_shape wide = s;  // the expanded pool: bf16, page i of request b at b * max_pages_per_seq + i
   wide.kv_dtype = DECATTN_KV_BF16;
   wide.num_pages = s.batch * s.max_pages_per_seq;
   const int32_t* wide_pt = reinterpret_cast<const int32_t*>(ws + off_pt);
   const int rc = prefill_enqueue(&wide, q, ws, ws + off_v, wide_pt, seq_lens, cu_q, total_rows, out, lse, status,
-                                 stream, /*check_only=*/true, /*bf16_out=*/true);
+                                 stream, /*check_only=*/true, splits, parts);
   if (rc != DECATTN_OK) return rc;
   WidenInt4Params w;
   w.k_codes = static_cast<const uint8_t*>(k_pages);
@@ -412,7 +435,7 @@ static int prefill_int4_enqueue(const dec_attn_shape* shape, const void* q, cons
   const cudaError_t e = launch_widen_int4(w, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail("INT4 prefill expansion launch", e);
   return prefill_enqueue(&wide, q, ws, ws + off_v, wide_pt, seq_lens, cu_q, total_rows, out, lse, status, stream,
-                         /*check_only=*/false, /*bf16_out=*/true);
+                         /*check_only=*/false, splits, parts);
 }
 
 }  // namespace decattn
@@ -422,9 +445,10 @@ using namespace decattn;
 extern "C" int64_t dec_attn_prefill_int4_workspace_bytes(const dec_attn_shape* shape) {
   if (!shape) return DECATTN_EINVAL;
   const dec_attn_shape& s = *shape;
-  if (s.batch < 0 || s.n_kv_heads <= 0 || s.page_size <= 0 || s.max_pages_per_seq < 0 || s.head_dim <= 0)
+  if (s.batch < 0 || s.n_kv_heads <= 0 || s.page_size <= 0 || s.max_pages_per_seq < 0 || s.head_dim <= 0 ||
+      s.n_q_heads <= 0 || s.n_q_heads % s.n_kv_heads != 0 || s.q_tokens <= 0)
     return DECATTN_EINVAL;
-  return widen_scratch_bytes(s.batch, s.max_pages_per_seq, s.n_kv_heads, s.page_size, s.head_dim, nullptr, nullptr);
+  return prefill_int4_scratch(s, nullptr, nullptr, nullptr, nullptr);
 }
 
 extern "C" int dec_attn_prefill_int4(const dec_attn_shape* shape, const void* q, const void* k_pages,

@@ -202,7 +202,18 @@ struct PrefillParams {
   float qk_scale_log2;        // sm_scale * log2(e)
   uint64_t wait_ns;           // a pipeline wait gives up after this long
   int32_t skip_fill;          // tests only: CTA 0's producer leaves this K block out (-1: none)
+  // bf16 output only: the keys of a request are split over up to `splits` CTAs (prefill_splits)
+  int splits;
+  float* part_o;              // [splits][total_rows][Hq][D] normalised partials
+  float* part_lse;            // [splits][total_rows][Hq]
 };
+
+// Key blocks of 128 that one CTA of a split prefill takes of a request with Lb keys; a row block that sees n
+// key blocks has ceil(n / that) parts. Short requests are split less: a part has four blocks at least.
+__host__ __device__ inline int prefill_part_blocks(int Lb, int splits) {
+  const int n = (Lb + 127) / 128, per = (n + splits - 1) / splits;
+  return per < 4 ? 4 : per;
+}
 
 // FP8 prefill: the E4M3 pages each request uses, widened to a bf16 scratch pool (prefill_fp8.cu).
 struct WidenParams {
@@ -509,7 +520,9 @@ bool split_int4_supported(int D, int GT);                         // split_int4.
 cudaError_t launch_split_int4(const SplitParams& p, int D, int device, cudaStream_t st);  // split_int4.cu
 cudaError_t launch_combine(const CombineParams& p, int device, cudaStream_t st);  // combine.cu
 cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
-                           const CUtensorMap& tmV, const CUtensorMap& tmO, cudaStream_t st);  // prefill.cu
+                           const CUtensorMap& tmV, const CUtensorMap& tmO, const CUtensorMap& tmP,
+                           cudaStream_t st);                      // prefill.cu
+int prefill_splits(int B, int T, int Hq, int G);                  // prefill.cu
 // bytes of the widened pool (K, then V at *off_v, then the page table at *off_pt)   prefill_fp8.cu
 int64_t widen_scratch_bytes(int B, int mpps, int Hkv, int P, int D, int64_t* off_v, int64_t* off_pt);
 cudaError_t launch_widen_kv(const WidenParams& p, cudaStream_t st);  // prefill_fp8.cu

@@ -155,12 +155,14 @@ __device__ __forceinline__ void pf_bulk_wait_read() {
 // Waits until every bulk group of this thread has completed (its global writes performed).
 __device__ __forceinline__ void pf_bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// BF16OUT: out is bf16 (rounded once from fp32), and a row that saw a NaN keeps it in lse; otherwise
-// out is fp32.
+// BF16OUT: out is bf16 (rounded once from fp32), a row that saw a NaN keeps it in lse, and the keys may be split
+// over p.splits CTAs (numbered between the row-block step and the request), whose fp32 parts
+// prefill_combine_kernel merges; otherwise out is fp32 and nothing is split.
 template <bool BF16OUT>
 __global__ void __launch_bounds__(kPfThreads, 1)
 prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO) {
+               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+               const __grid_constant__ CUtensorMap tmP) {
   using L = PfSmem;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -169,13 +171,16 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
   volatile int* abort = reinterpret_cast<volatile int*>(sm + L::OFF_MISC + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t wl = p.wait_ns;  // every pipeline wait gives up after this long
+  if (BF16OUT) griddep_wait();    // launched while the pages are still being expanded
 
   // ---- request, KV head and the two tiles of this CTA. The row-block step is the slowest
   //      index of the grid, counted down, so the CTAs with the most keys start first.
   const bool head_pair = (p.G % 2) == 0;
   const int ny = head_pair ? p.Hq / 2 : p.Hq;
   const int nsteps = head_pair ? pf_tiles_per_head(p.T) : (pf_tiles_per_head(p.T) + 1) / 2;
-  const int step = nsteps - 1 - (int)blockIdx.x / (p.B * ny);
+  const int nsplit = BF16OUT ? p.splits : 1;
+  const int step = nsteps - 1 - (int)blockIdx.x / (p.B * ny * nsplit);
+  const int split = (int)blockIdx.x / (p.B * ny) % nsplit;
   const int rem = (int)blockIdx.x % (p.B * ny);
   const int b = rem / ny, y = rem % ny;
   const int Lb = p.seq_lens[b];
@@ -211,6 +216,17 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
     return;
   }
   const int h = tl0.qh / p.G;
+  // this CTA's part of the keys: blocks kb0 .. of both tiles; a tile of one part is written as it is
+  int kb0 = 0, parts0 = 1, parts1 = 1;
+  if (BF16OUT && nsplit > 1) {
+    const int per = prefill_part_blocks(max(Lb, 0), nsplit);
+    kb0 = split * per;
+    parts0 = max((tl0.nkb + per - 1) / per, 1);
+    parts1 = max((tl1.nkb + per - 1) / per, 1);
+    if (split >= max(parts0, parts1)) return;
+    tl0.nkb = min(max(tl0.nkb - kb0, 0), per);
+    tl1.nkb = min(max(tl1.nkb - kb0, 0), per);
+  }
   const int nkb_max = max(tl0.nkb, tl1.nkb);
 
   if (threadIdx.x == 0) {
@@ -264,7 +280,7 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
       const int st = g % kPfStages;
       const uint32_t eph = (uint32_t)((g / kPfStages) & 1) ^ 1u;
       // lane i < 8: the 16-key group i of the block (its page id and row in the pool)
-      const int key16 = g * kPfN + 16 * lane;
+      const int key16 = (kb0 + g) * kPfN + 16 * lane;
       const bool has = lane < kPfN / 16 && key16 < Lb;
       int row = 0;
       if (has) {
@@ -413,7 +429,7 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
     for (int g = 0; g < nkb; ++g) {
       if (!tc_wait_suspend_warp(&bar[kPfSFull + u], (uint32_t)(g & 1), p.status, abort, wl)) { ok = false; break; }
       tc_fence_after();
-      const int j0 = g * kPfN;
+      const int j0 = (kb0 + g) * kPfN;
       const bool masked = j0 + kPfN - 1 > lim_min;  // warp-uniform: some row does not see every key
       const int nvis = lim - j0 + 1;                // keys j0 .. j0 + nvis - 1 are visible to the row
       // the row's 128 scores in registers; keys past the row's limit are invisible
@@ -474,7 +490,14 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
       const bool whole_box = t0w + 32 <= Tb;
       const float inv = (BF16OUT ? l != 0.f : l > 0.f) ? 1.f / l : 0.f;
       uint8_t* stage = sm + L::OFF_Q + warp * 8192;
-      if (BF16OUT) {
+      const int parts = u ? parts1 : parts0;
+      const bool part = BF16OUT && parts > 1;  // one of several: fp32, rows behind those of the parts before
+      const int64_t prow = part ? (int64_t)split * p.total_rows : 0;
+      float* const out_f = part ? p.part_o : p.out;
+      float* const lse_f = part ? p.part_lse : p.lse;
+      if (split >= parts) {
+        // this tile has no such part
+      } else if (BF16OUT && !part) {
         // two boxes of 32 rows x 64 head dims, one per 4 KB half of the staging area
         #pragma unroll
         for (int q2 = 0; q2 < kPfD / 64; ++q2) {
@@ -523,7 +546,7 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
           }
           if (!whole_box) {
             if (t < Tb) {
-              float4* dst = reinterpret_cast<float4*>(p.out + ((int64_t)(qoff + t) * p.Hq + qh) * kPfD + 32 * q4);
+              float4* dst = reinterpret_cast<float4*>(out_f + ((prow + qoff + t) * p.Hq + qh) * kPfD + 32 * q4);
               #pragma unroll
               for (int c = 0; c < 8; ++c)
                 dst[c] = make_float4(o[4 * c] * inv, o[4 * c + 1] * inv, o[4 * c + 2] * inv, o[4 * c + 3] * inv);
@@ -542,15 +565,15 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            pf_tma_store_3d(&tmO, box, 32 * q4, qh, qoff + t0w);
+            pf_tma_store_3d(part ? &tmP : &tmO, box, 32 * q4, qh, (int)prow + qoff + t0w);
             pf_bulk_commit();
           }
         }
       }
       if (lane == 0) pf_bulk_wait_all();
       __syncwarp();
-      if (t < Tb)
-        p.lse[(int64_t)(qoff + t) * p.Hq + qh] =
+      if (t < Tb && split < parts)
+        lse_f[(prow + qoff + t) * p.Hq + qh] =
             (BF16OUT ? l != 0.f : l > 0.f) ? (mref + __log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
   }
@@ -562,20 +585,95 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kPfTmemCols) : "memory");
 }
 
+// The parts of a split prefill into the output: a warp takes one (packed row, q head), lane l head dims
+// 4 l .. 4 l + 3. Rows of one part were written by their CTA; rows behind the last request are left alone.
+constexpr int kPfcThreads = 256;
+
+__global__ void __launch_bounds__(kPfcThreads) prefill_combine_kernel(const PrefillParams p) {
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t item = (int64_t)blockIdx.x * (kPfcThreads / 32) + (threadIdx.x >> 5);
+  if (item >= p.total_rows * p.Hq) return;
+  const int row = (int)(item / p.Hq);
+  int b, c0, Tb;
+  if (p.cu_q) {
+    if (row >= p.cu_q[p.B]) return;
+    int a = 0, z = p.B - 1;  // last request with cu_q[b] <= row
+    while (a < z) {
+      const int mid = (a + z + 1) >> 1;
+      if (p.cu_q[mid] <= row) a = mid; else z = mid - 1;
+    }
+    b = a;
+    c0 = p.cu_q[b];
+    Tb = p.cu_q[b + 1] - c0;
+    if (c0 < 0 || row < c0 || Tb > p.T || (int64_t)c0 + Tb > p.total_rows) return;  // reported, not written
+  } else {
+    b = row / p.T;
+    c0 = b * p.T;
+    Tb = p.T;
+  }
+  const int t = row - c0, Lb = p.seq_lens[b];
+  const int tlast = min(t / kPfM * kPfM + kPfM, Tb) - 1;
+  const int nkb = Lb < 0 ? 0 : (max(0, min(Lb, Lb - Tb + tlast + 1)) + kPfN - 1) / kPfN;  // of the row's block
+  const int per = prefill_part_blocks(max(Lb, 0), p.splits);
+  const int parts = (nkb + per - 1) / per;
+  if (parts <= 1) return;
+  const int64_t stride = p.total_rows * p.Hq;
+  const float my = lane < parts ? p.part_lse[lane * stride + item] : -INFINITY;  // at most 16 parts
+  float M = my;
+  #pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float wgt = M == -INFINITY ? 0.f : expf(my - M);
+  if (my != my) wgt = my;  // fmaxf leaves NaNs out of M
+  float W = wgt;
+  #pragma unroll
+  for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < parts; ++s) {
+    const float w = __shfl_sync(0xffffffffu, wgt, s);
+    const float4 v = reinterpret_cast<const float4*>(p.part_o + (s * stride + item) * kPfD)[lane];
+    acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
+  }
+  const float inv = W == 0.f ? 0.f : 1.f / W;
+  reinterpret_cast<uint2*>(p.out_bf16 + item * kPfD)[lane] =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (lane == 0) p.lse[item] = W == 0.f ? -INFINITY : M + logf(W);
+}
+
+// Parts that the keys are split into at most: as many as bring the grid to four CTAs per multiprocessor of a B200
+// (the parts differ in length: the heaviest come first and the light ones fill up), 16 at most.
+int prefill_splits(int B, int T, int Hq, int G) {
+  const int64_t grid = pf_grid(B, T, Hq, G);
+  if (grid <= 0) return 1;
+  const int64_t n = (4 * 148 + grid - 1) / grid;
+  return (int)(n > 16 ? 16 : n);
+}
+
 cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
-                           const CUtensorMap& tmV, const CUtensorMap& tmO, cudaStream_t st) {
+                           const CUtensorMap& tmV, const CUtensorMap& tmO, const CUtensorMap& tmP, cudaStream_t st) {
   const int smem = PfSmem::ALLOC;
   const auto fn = p.out_bf16 ? prefill_kernel<true> : prefill_kernel<false>;
   if (!ensure_smem_attr((const void*)fn, smem)) return cudaErrorInvalidValue;
   if (p.B == 0 || p.T == 0 || p.Hq == 0) return cudaSuccess;
-  const int64_t grid = (int64_t)pf_grid(p.B, p.T, p.Hq, p.G);
+  const int64_t grid = (int64_t)pf_grid(p.B, p.T, p.Hq, p.G) * (p.out_bf16 ? p.splits : 1);
   if (grid <= 0 || grid > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kPfThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  return cudaLaunchKernelEx(&cfg, fn, p, tmQ, tmK, tmV, tmO);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see griddep_wait in the kernels
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.out_bf16 ? 1 : 0;
+  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p, tmQ, tmK, tmV, tmO, tmP); e != cudaSuccess) return e;
+  if (!p.out_bf16 || p.splits == 1) return cudaSuccess;
+  const int64_t items = p.total_rows * p.Hq;
+  cfg.gridDim = dim3((unsigned)((items + kPfcThreads / 32 - 1) / (kPfcThreads / 32)));
+  cfg.blockDim = dim3(kPfcThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, prefill_combine_kernel, p);
 }
 
 }  // namespace decattn

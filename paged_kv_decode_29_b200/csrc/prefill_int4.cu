@@ -23,6 +23,8 @@ constexpr int kWiD = 128;
 // are left unwritten; the rows past its last key, up to a multiple of 16, are zero. A page id outside
 // the pool is reported (DECATTN_EDEVICE) and its scratch page is zero.
 __global__ void __launch_bounds__(kWiThreads) widen_int4_kernel(const WidenInt4Params p) {
+  griddep_wait();               // the pages were written by earlier kernels of the stream
+  griddep_launch_dependents();  // the prefill kernel may be scheduled; it waits for this grid itself
   const int w = (int)blockIdx.x, h = (int)blockIdx.y;
   const int b = w / p.mpps, i = w - b * p.mpps;
   if (threadIdx.x == 0 && h == 0) p.pt_out[w] = w;
@@ -63,8 +65,16 @@ cudaError_t launch_widen_int4(const WidenInt4Params& p, cudaStream_t st) {
   const int64_t grid = (int64_t)p.B * p.mpps;
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff || p.Hkv > 65535) return cudaErrorInvalidValue;
-  widen_int4_kernel<<<dim3((unsigned)grid, (unsigned)p.Hkv), kWiThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)p.Hkv);
+  cfg.blockDim = dim3(kWiThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // launched while the previous kernel drains
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, widen_int4_kernel, p);
 }
 
 }  // namespace decattn

@@ -394,7 +394,8 @@ def _prefill(cache, q, rows, *, uniform, max_rows=None, pad=0, sm_scale=0.0, exp
     lead = (len(rows), rows[0]) if uniform else (n + pad,)
     ob = torch.full(((n + pad) * hq * 128 + 128,), 5.0, dtype=torch.bfloat16, device="cuda")
     lb = torch.full(((n + pad) * hq + 64,), 5.0, dtype=torch.float32, device="cuda")
-    ws = torch.full((da.prefill_int4_workspace_bytes(dev["k"], dev["tab"]) + 256,), CANARY, dtype=torch.uint8, device="cuda")
+    need = da.prefill_int4_workspace_bytes(lead + (hq, 128), dev["k"], dev["tab"], max_rows or max(rows))
+    ws = torch.full((need + 256,), CANARY, dtype=torch.uint8, device="cuda")
     st = torch.zeros((), dtype=torch.int32, device="cuda")
     if cu is None and not uniform:
         cu = np.concatenate(([0], np.cumsum(rows)))
@@ -434,6 +435,7 @@ def test_prefill_uniform_matches_64_bit_attention(hq, hkv, P, lens, T):
 @pytest.mark.parametrize("lens,rows,pad", [
     ([300, 40, 129], [1, 40, 129], 0),
     ([500, 20, 0, 64], [160, 0, 3, 64], 37),  # no rows; rows without a key; a padded batch
+    ([5000, 700, 130], [257, 130, 1], 3),     # keys split over CTAs: many parts, few, one
 ])
 def test_prefill_packed_matches_64_bit_attention(lens, rows, pad):
     cache = I4.Cache(lens, Hkv=2, d=128, P=16, seed=41 + pad)
@@ -467,19 +469,20 @@ def test_prefill_nan_rows_bad_pages_and_offsets():
 
 
 def test_prefill_is_the_bf16_prefill_over_the_caches_values():
-    """The same kernel over the same numbers: equal to dec_attn_prefill over the values, rounded to bf16."""
-    lens, T = [400, 333], 200
+    """Where the keys are not split: the same kernel over the same numbers, so equal to dec_attn_prefill over the
+    values, rounded to bf16."""
+    lens, T, hq = [400, 333], 200, 592
     cache = I4.Cache(lens, Hkv=2, d=128, P=16, seed=45)
-    q = I4.bf16(np.random.default_rng(46).standard_normal((2 * T, 8, 128)))
+    q = I4.bf16(np.random.default_rng(46).standard_normal((2 * T, hq, 128)))
     out, lse = _prefill(cache, q, [T, T], uniform=True)
     dev = cache.to_device()
     for b, L in enumerate(lens):                             # the bf16 pools need numbers behind the last key
         pid, used = cache.table[b, (L - 1) // 16], (L - 1) % 16 + 1
         cache.words[:, pid, :, used:] = 0x3F80
     pools = [_bf16_dev(np.nan_to_num(I4.values(cache.pools[w], cache.words[w]), posinf=0, neginf=0)) for w in (0, 1)]
-    o2, l2 = da.prefill(_bf16_dev(q).view(2, T, 8, 128), pools[0], pools[1], dev["tab"], dev["lens"])
-    assert np.array_equal(_f64(l2).reshape(-1, 8), lse)
-    assert np.array_equal(_f64(o2.to(torch.bfloat16)).reshape(-1, 8, 128), out)
+    o2, l2 = da.prefill(_bf16_dev(q).view(2, T, hq, 128), pools[0], pools[1], dev["tab"], dev["lens"])
+    assert np.array_equal(_f64(l2).reshape(-1, hq), lse)
+    assert np.array_equal(_f64(o2.to(torch.bfloat16)).reshape(-1, hq, 128), out)
 
 
 def test_prefill_wait_runs_out_then_the_context_is_usable():

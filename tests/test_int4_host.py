@@ -167,8 +167,12 @@ def test_prefill_host_checks(lib):
     s = _shape(q_tokens=300)
     B, mpps, Hkv, P = s.batch, s.max_pages_per_seq, s.n_kv_heads, s.page_size
     kv = -(-(B * mpps * Hkv * P * 128 * 2) // 256) * 256
+    pools = 2 * kv + -(-(B * mpps * 4) // 256) * 256
     need = lib.dec_attn_prefill_int4_workspace_bytes(C.byref(s))
-    assert need == 2 * kv + -(-(B * mpps * 4) // 256) * 256
+    assert need == pools + 16 * (B * 300 * 8 * 129 * 4)              # 24 CTAs: 16 parts
+    many = _shape(q_tokens=300, n_q_heads=592)                       # a grid that fills the GPU: no parts
+    assert lib.dec_attn_prefill_int4_workspace_bytes(C.byref(many)) == pools
+    assert lib.dec_attn_prefill_int4_workspace_bytes(C.byref(_shape(q_tokens=0))) == da.EINVAL
     assert lib.dec_attn_prefill_int4_workspace_bytes(None) == da.EINVAL
     assert lib.dec_attn_prefill_int4_workspace_bytes(C.byref(_shape(batch=-1))) == da.EINVAL
 
@@ -185,6 +189,7 @@ def test_prefill_host_checks(lib):
                      (dict(batch=70000), da.ENOTSUP)):
         assert call(_shape(**{**dict(q_tokens=300), **kw}), ws_bytes=1 << 60) == code
     assert call(s, total=5) == da.EINVAL
+    assert call(s, total=601, cu=FAKE) == da.EINVAL                  # more rows than batch * q_tokens
     for name in ("q", "k", "v", "w", "tab", "lens", "ws", "out", "lse"):
         assert call(s, **{name: None}) == da.EINVAL
     for name in ("q", "k", "v", "w", "ws", "out"):
