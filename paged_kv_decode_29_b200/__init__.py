@@ -460,6 +460,9 @@ def prefill_fp8_workspace_bytes(q_shape, k_pages: torch.Tensor, page_table: torc
     return n
 
 
+_INT4_PLACE = "every tensor must be contiguous and on the current CUDA device"
+
+
 def _int4_args(rows: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_words: torch.Tensor,
                page_table: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch.Tensor | None, *others):
     """The shape of a call over an INT4 cache and its total rows, after the checks that only the tensors allow.
@@ -492,9 +495,14 @@ def _int4_args(rows: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
             or kv_words.shape != (2,) + pool_shape[:3]):
         raise ValueError("an INT4 cache is k_pages / v_pages [num_pages][Hkv][P][d / 2], kv_words [2][num_pages][Hkv][P]")
     dev = torch.cuda.current_device()
-    for t in (rows, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, *others):
+    if not (rows.get_device() == k_pages.get_device() == v_pages.get_device() == kv_words.get_device() == dev
+            and page_table.get_device() == seq_lens.get_device() == dev and rows.is_contiguous()
+            and k_pages.is_contiguous() and v_pages.is_contiguous() and kv_words.is_contiguous()
+            and page_table.is_contiguous() and seq_lens.is_contiguous()):
+        raise ValueError(_INT4_PLACE)
+    for t in others if cu_q_lens is None else (cu_q_lens, *others):
         if t is not None and (t.get_device() != dev or not t.is_contiguous()):
-            raise ValueError("every tensor must be contiguous and on the current CUDA device")
+            raise ValueError(_INT4_PLACE)
     return ShapeT(B, q_shape[-2], pool_shape[1], q_shape[-1], T, pool_shape[2], pool_shape[0], mpps, KV_INT4, 0.0), total
 
 

@@ -514,7 +514,10 @@ extern "C" int dec_attn_default_tile_len(int batch, int n_kv_heads, int64_t tota
   const double tile_cost = 8192.0;  // fixed cost of a tile (q, epilogue, pipeline start) in KV-byte terms
   int best = 0;
   double best_est = 0.0;
-  for (int tl = page_size; tl <= 8192; tl *= 2) {
+  // the INT4 kernel takes 64 keys at a time: a shorter tile saves it nothing
+  int shortest = page_size;
+  while (kv_dtype == DECATTN_KV_INT4 && shortest < 64) shortest *= 2;
+  for (int tl = shortest; tl <= 8192; tl *= 2) {
     const double U = W / tl;  // tiles, as if every tile were full
     const double per_bin = U > 0 ? ceil(U / N) : 0.0;
     // the busiest bin's KV bytes and tile overheads, plus the partials every tile writes and the

@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(kCombineThreads, kCombineCtasPerSm) combine_ke
 
 cudaError_t launch_combine(const CombineParams& p, int device, cudaStream_t st) {
   if ((int64_t)p.B * p.T * p.Hq <= 0) return cudaSuccess;
-  int sms = 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return cudaErrorUnknown;
+  const int sms = default_bins(device) / split_ctas_per_sm();
+  if (sms <= 0) return cudaErrorUnknown;
   if (p.D != 128 && p.D != 64) return cudaErrorInvalidValue;
   auto pick = [&](auto bf16) -> const void* {
     constexpr bool BF = decltype(bf16)::value;
@@ -271,7 +271,7 @@ cudaError_t launch_combine(const CombineParams& p, int device, cudaStream_t st) 
   const void* fn = p.out_bf16 ? pick(std::true_type{}) : pick(std::false_type{});
   const int64_t nu = p.sparse ? (int64_t)p.B * p.Hkv : p.B;
   const int smem = nu <= kCombineSmemRequests ? (int)(4 * (2 * (nu + 1) + p.B + 1)) : 0;
-  if (!ensure_smem_attr(fn, smem)) return cudaErrorInvalidValue;
+  if (smem > 48 * 1024 && !ensure_smem_attr(fn, smem)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms * kCombineCtasPerSm);
   cfg.blockDim = dim3(kCombineThreads);

@@ -641,7 +641,8 @@ __global__ void __launch_bounds__(kPfcThreads) prefill_combine_kernel(const Pref
 }
 
 // Parts that the keys are split into at most: as many as bring the grid to four CTAs per multiprocessor of a B200
-// (the parts differ in length: the heaviest come first and the light ones fill up), 16 at most.
+// (they differ in length: the heaviest come first, short ones fill up), 16 at most. On 5 ragged chunks (a grid
+// of 200): 137 us in one part, 104 in three, 111 in eight (more parts to write and merge).
 int prefill_splits(int B, int T, int Hq, int G) {
   const int64_t grid = pf_grid(B, T, Hq, G);
   if (grid <= 0) return 1;

@@ -19,6 +19,9 @@
 // all keys: every code is decoded once, a lane holds 8 NQ numbers of O for 8 NQ query rows, and nothing is merged
 // at a tile's end. X goes from the warps that have the scores to all warps through shared memory (stmatrix.trans
 // turns it into the B operand's layout).
+// More than 16 query rows go to several CTAs, 16 rows each, which walk the same bins side by side (neighbours in the
+// grid: K and V come from L2 for all but one). They decode every code again, but run 16 warps a multiprocessor.
+// 25 rows a KV head over 35091 keys, head_dim 64: MEASURED
 //  * One barrier per block, after its scores. It carries a vote whether a score or a V scale passes the
 //    references (m by more than 2^kI4Tau, s^V at all); if so the CTA takes the exact maxima, else they stay.
 //    It also makes X of the block before visible, whose product comes next, beside the exponentials of this one.
@@ -127,8 +130,11 @@ split_int4_kernel(const SplitParams p) {
     p.row_cnt[i] = 0;
 
   // ======================================================================= tiles
-  // The CTA's tiles: those of bins blockIdx.x, + gridDim.x, ..., numbered through; descriptor u at queue[u % 64].
-  int bin = (int)blockIdx.x, bin_j = 0;  // warp 0: the next descriptor to fetch
+  // The CTA's query rows: r0 .. of every KV head. Its tiles: those of bins blockIdx.x / groups, + gridDim.x / groups,
+  // ..., numbered through; descriptor u at queue[u % 64].
+  const int groups = (p.GT + 8 * NQ - 1) / (8 * NQ);
+  const int r0 = 8 * NQ * ((int)blockIdx.x % groups);
+  int bin = (int)blockIdx.x / groups, bin_j = 0;  // warp 0: the next descriptor to fetch
   int total = 0;                         // descriptors fetched so far
   bool last = false;                     // there are no more
   int refills = 0;
@@ -149,7 +155,7 @@ split_int4_kernel(const SplitParams p) {
           bin_j += max(n, 0);
           if (n <= 0) {
             n = 0;
-            bin += (int)gridDim.x;
+            bin += (int)gridDim.x / groups;
             bin_j = 0;
           }
         }
@@ -258,8 +264,22 @@ split_int4_kernel(const SplitParams p) {
   const uint32_t x_rd = C::OFF_X + (lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
   const float LN2 = 0.6931471805599453f;
 
+  // q of a tile: D / 8 lanes take a row, 8 head dims each
+  constexpr int LPQ = D / 8, RPP = 32 / LPQ, PASSES = 8 * NQ / W / RPP;
+  uint4 qx[PASSES];
+  auto load_q = [&](const Unit& u) {
+    #pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const int r = r0 + (w * PASSES + i) * RPP + lane / LPQ, t = r / p.G, g = r - t * p.G;
+      qx[i] = make_uint4(0, 0, 0, 0);
+      if (r < p.GT)
+        qx[i] = *reinterpret_cast<const uint4*>(p.q + (((int64_t)u.b * p.T + t) * p.Hq + (int64_t)u.h * p.G + g) * D + 8 * (lane % LPQ));
+    }
+  };
+
   fetch_chunk();
   if (f_unit < 0) return;  // no tile
+  load_q(queue[0]);        // beside the first copies
   #pragma unroll
   for (int i = 0; i < kI4Stages; ++i) copy_step(i, i >= 2);
   cp_async_wait<kI4Stages - 1>();
@@ -279,28 +299,19 @@ split_int4_kernel(const SplitParams p) {
     //      32 c + 8 tig .. + 7 of chunk c: the pairs (i, i + 4) of those eight in register i, as the codes of K's
     //      words pair up, those that meet a code times 16 over 16. Here D / 8 lanes take a row, 8 head dims each.
     {
-      constexpr int LPQ = D / 8, RPP = 32 / LPQ, PASSES = 8 * NQ / W / RPP;
-      uint4 x[PASSES];
-      #pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const int r = (w * PASSES + i) * RPP + lane / LPQ, t = r / p.G, g = r - t * p.G;
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (r < p.GT)
-          x[i] = *reinterpret_cast<const uint4*>(p.q + (((int64_t)d.b * p.T + t) * p.Hq + (int64_t)d.h * p.G + g) * D + 8 * (lane % LPQ));
-      }
       #pragma unroll
       for (int i = 0; i < PASSES; ++i) {
         const int row = (w * PASSES + i) * RPP + lane / LPQ, sg = lane % LPQ;
         // largest bit pattern without its sign: infinities and NaNs come out on top
-        uint32_t amax = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                 __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+        uint32_t amax = __vmaxu2(__vmaxu2(qx[i].x & 0x7fff7fffu, qx[i].y & 0x7fff7fffu),
+                                 __vmaxu2(qx[i].z & 0x7fff7fffu, qx[i].w & 0x7fff7fffu));
         amax = max(amax & 0xffffu, amax >> 16);
         #pragma unroll
         for (int k = 1; k < LPQ; k <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, k));
         const int E = amax == 0 ? 0 : min(max(14 + 127 - (int)(amax >> 7), -100), 100);
         const float up = __int_as_float((127 + E) << 23);
-        float v[8] = {bf16_lo(x[i].x), bf16_hi(x[i].x), bf16_lo(x[i].y), bf16_hi(x[i].y),
-                      bf16_lo(x[i].z), bf16_hi(x[i].z), bf16_lo(x[i].w), bf16_hi(x[i].w)};
+        float v[8] = {bf16_lo(qx[i].x), bf16_hi(qx[i].x), bf16_lo(qx[i].y), bf16_hi(qx[i].y),
+                      bf16_lo(qx[i].z), bf16_hi(qx[i].z), bf16_lo(qx[i].w), bf16_hi(qx[i].w)};
         float sum = 0.f;
         #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -342,7 +353,7 @@ split_int4_kernel(const SplitParams p) {
         nmu[nw][e] = lrow[nw][e] = zrow[nw][e] = 0.f;
       }
     // key j is visible to query token t if j <= Lb - T + t: keys below this need no mask in any row
-    const int safe_end = min(d.tok_end, d.seq_len - p.T + 1);
+    const int safe_end = min(d.tok_end, d.seq_len - p.T + r0 / p.G + 1);
 
     // O^T += V^T X^T over the 64 keys at a place of the V ring, X in buffer xs
     auto product = [&](uint32_t place, int xs) {
@@ -430,7 +441,7 @@ split_int4_kernel(const SplitParams p) {
           const bool bad = vsc[mt][i >> 1] != vsc[mt][i >> 1];
           #pragma unroll
           for (int nw = 0; nw < NQ; ++nw) {
-            const int r = 8 * nw + 2 * tig + (i & 1), j = j0 + (i >> 1) * 8;
+            const int r = r0 + 8 * nw + 2 * tig + (i & 1), j = j0 + (i >> 1) * 8;
             if (j >= d.tok_end || (r < p.GT && j > d.seq_len - p.T + r / p.G)) sv[mt][nw][i] = -INFINITY;
             else if (bad) sv[mt][nw][i] = vsc[mt][i >> 1];
           }
@@ -586,6 +597,7 @@ split_int4_kernel(const SplitParams p) {
     __syncthreads();
     product((g - 1) % kI4Stages, (nblk - 1) & 1);
 
+    if (unit + 1 <= f_unit) load_q(queue[(unit + 1) % kI4Queue]);  // beside the epilogue
     // ---- epilogue: normalise, store. O is in units of 2^(eref - 127 - kI4XExp): codes and X exactly so
     const float unref = __int_as_float((eref - kI4XExp) << 23);  // eref >= 16
     #pragma unroll
@@ -598,7 +610,7 @@ split_int4_kernel(const SplitParams p) {
           l += xsum[i * 16 * NQ + 8 * nw + 2 * tig + e];
           z += xsum[i * 16 * NQ + 8 * NQ + 8 * nw + 2 * tig + e];
         }
-        const int r = 8 * nw + 2 * tig + e;
+        const int r = r0 + 8 * nw + 2 * tig + e;
         if (r >= p.GT) continue;
         const float inv = l == 0.f ? 0.f : unref / l;
         const float lse_v = l == 0.f ? -INFINITY : (__log2f(l) - nmu[nw][e]) * LN2;
@@ -627,7 +639,9 @@ static cudaError_t launch_i4(const SplitParams& p, int sms, cudaStream_t st) {
   auto fn = split_int4_kernel<D, NQ, CPS>;
   if (!ensure_smem_attr((const void*)fn, C::ALLOC)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.n_bins < sms * CPS ? p.n_bins : sms * CPS);
+  const int groups = (p.GT + 8 * NQ - 1) / (8 * NQ);
+  const int n = sms * CPS / groups;  // bins at a time
+  cfg.gridDim = dim3((p.n_bins < n ? p.n_bins : n) * groups);
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::ALLOC;
   cfg.stream = st;
@@ -641,10 +655,7 @@ static cudaError_t launch_i4(const SplitParams& p, int sms, cudaStream_t st) {
 
 template <int D>
 static cudaError_t launch_i4_gt(const SplitParams& p, int sms, cudaStream_t st) {
-  if (p.GT <= 8) return launch_i4<D, 1, 4>(p, sms, st);
-  if (p.GT <= 16) return launch_i4<D, 2, 4>(p, sms, st);
-  if (p.GT <= 32) return launch_i4<D, 4, 2>(p, sms, st);
-  return launch_i4<D, 8, 2>(p, sms, st);
+  return p.GT <= 8 ? launch_i4<D, 1, 4>(p, sms, st) : launch_i4<D, 2, 4>(p, sms, st);
 }
 
 bool split_int4_supported(int D, int GT) { return GT >= 1 && GT <= kMaxGT && (D == 64 || D == 128); }

@@ -206,6 +206,7 @@ def test_default_tile_len_of_int4(lib):
     for P in (16, 32, 48, 256):
         tl = f(8, 8, 100000, P, 128, 4, da.KV_INT4, 592)
         assert tl > 0 and tl % P == 0
+    assert f(2, 2, 822, 16, 128, 4, da.KV_INT4, 592) == 64           # tiny: one block of the kernel
     # fewer bytes per key than E4M3: a tile is never shorter
     for total in (2000, 40000, 500000):
         assert f(8, 8, total, 16, 128, 4, da.KV_INT4, 592) >= f(8, 8, total, 16, 128, 4, da.KV_FP8E4M3, 592)
