@@ -511,7 +511,9 @@ extern "C" int dec_attn_default_tile_len(int batch, int n_kv_heads, int64_t tota
   const double elem = kv_dtype == DECATTN_KV_BF16 ? 2.0 : kv_dtype == DECATTN_KV_INT4 ? 0.5 + 2.0 / head_dim : 1.0;
   const double N = (double)n_bins;
   const double W = (double)n_kv_heads * (double)total_kv_tokens;  // token-heads of the step
-  const double tile_cost = 8192.0;  // fixed cost of a tile (q, epilogue, pipeline start) in KV-byte terms
+  // fixed cost of a tile (q, epilogue, pipeline start) in KV-byte terms; the INT4 kernel decodes half the bytes
+  // of E4M3 in about the time of two blocks of 64 keys
+  const double tile_cost = kv_dtype == DECATTN_KV_INT4 ? 16384.0 : 8192.0;
   int best = 0;
   double best_est = 0.0;
   // the INT4 kernel takes 64 keys at a time: a shorter tile saves it nothing

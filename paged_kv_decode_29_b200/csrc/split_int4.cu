@@ -62,7 +62,7 @@ struct I4Cfg {
   static constexpr int OFF_QFRAG = OFF_X + 2 * XBUF;
   static constexpr int OFF_QUEUE = OFF_QFRAG + QFRAG;
   static constexpr int OFF_XCH = OFF_QUEUE + kI4Queue * (int)sizeof(Unit);
-  static constexpr int XCH = 4 * (W * 3 * 8 * NQ + 2 * 8 * NQ + W + 2);  // see the pointers into it
+  static constexpr int XCH = 4 * (W * 3 * 8 * NQ + 3 * 8 * NQ + W + 2);  // see the pointers into it
   static constexpr int BYTES = (OFF_XCH + XCH + 15) / 16 * 16;
   static constexpr int ALLOC = BYTES + 128;                   // slack to align the base to 128
   // byte offset of (row r, 16-byte chunk c) in a block's K or V codes: the chunks of rows 64 or 32 bytes long are
@@ -116,9 +116,9 @@ split_int4_kernel(const SplitParams p) {
   const uint32_t smb = smem_u32(sm);
   Unit* queue = reinterpret_cast<Unit*>(sm + C::OFF_QUEUE);
   float* xmax = reinterpret_cast<float*>(sm + C::OFF_XCH);  // [warp][8 NQ]
-  float* xsum = xmax + W * 8 * NQ;                          // [warp][l, zero points][8 NQ]
-  float* qrow = xsum + W * 2 * 8 * NQ;                      // [score factor, <1, q>][8 NQ]
-  int* xexp = reinterpret_cast<int*>(qrow + 2 * 8 * NQ);    // [warp]
+  float* xsum = xmax + W * 8 * NQ;                          // [l, zero points][8 NQ][warp]
+  float* qrow = xsum + W * 2 * 8 * NQ;                      // [score factor, <1, q>, one over the factor][8 NQ]
+  int* xexp = reinterpret_cast<int*>(qrow + 3 * 8 * NQ);    // [warp]
   int* n_queued = xexp + W;                                 // [2]: of every other refill
   // Everything below reads or writes what earlier kernels of the stream may still be working on: the
   // plan, the pages (a plan serves every layer of a step, so the kernel before this one can be the
@@ -266,16 +266,26 @@ split_int4_kernel(const SplitParams p) {
 
   // q of a tile: D / 8 lanes take a row, 8 head dims each
   constexpr int LPQ = D / 8, RPP = 32 / LPQ, PASSES = 8 * NQ / W / RPP;
+  // query row r of a KV head is row (r / G) Hq + r % G behind the first one of (request, head); -1: no such row
+  auto row_of = [&](int r) { return r < p.GT ? r / p.G * p.Hq + r % p.G : -1; };
+  auto first_row = [&](const Unit& u) { return (int64_t)u.b * p.T * p.Hq + (int64_t)u.h * p.G; };
   uint4 qx[PASSES];
+  int q_rows[PASSES];
+  #pragma unroll
+  for (int i = 0; i < PASSES; ++i) q_rows[i] = row_of(r0 + (w * PASSES + i) * RPP + lane / LPQ);
   auto load_q = [&](const Unit& u) {
+    const uint16_t* src = p.q + first_row(u) * D + 8 * (lane % LPQ);
     #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-      const int r = r0 + (w * PASSES + i) * RPP + lane / LPQ, t = r / p.G, g = r - t * p.G;
       qx[i] = make_uint4(0, 0, 0, 0);
-      if (r < p.GT)
-        qx[i] = *reinterpret_cast<const uint4*>(p.q + (((int64_t)u.b * p.T + t) * p.Hq + (int64_t)u.h * p.G + g) * D + 8 * (lane % LPQ));
+      if (q_rows[i] >= 0) qx[i] = *reinterpret_cast<const uint4*>(src + (int64_t)q_rows[i] * D);
     }
   };
+  int o_rows[NQ][2];  // of this lane's columns of O^T
+  #pragma unroll
+  for (int nw = 0; nw < NQ; ++nw)
+    #pragma unroll
+    for (int e = 0; e < 2; ++e) o_rows[nw][e] = row_of(r0 + 8 * nw + 2 * tig + e);
 
   fetch_chunk();
   if (f_unit < 0) return;  // no tile
@@ -324,8 +334,10 @@ split_int4_kernel(const SplitParams p) {
         #pragma unroll
         for (int k = 1; k < LPQ; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
         if (sg == 0) {  // a row that is not finite has NaN scores
-          qrow[row] = amax >= 0x7f80u ? __int_as_float(0x7fc00000) : __int_as_float((127 + 24 - E) << 23) * p.qk_scale_log2;
+          const float f = amax >= 0x7f80u ? __int_as_float(0x7fc00000) : __int_as_float((127 + 24 - E) << 23) * p.qk_scale_log2;
+          qrow[row] = f;
           qrow[8 * NQ + row] = sum * 0x1p-24f;
+          qrow[16 * NQ + row] = 1.f / f;
         }
       }
     }
@@ -512,7 +524,7 @@ split_int4_kernel(const SplitParams p) {
           const float mu = mnew == -INFINITY ? 0.f : mnew;
           const float alpha = fast_exp2(mold - mu);
           nmu[nw][e] = -mu;
-          thr[nw][e] = mnew == -INFINITY ? -INFINITY : (mnew + (float)kI4Tau) / fcol[nw][e];
+          thr[nw][e] = mnew == -INFINITY ? -INFINITY : (mnew + (float)kI4Tau) * qrow[16 * NQ + 8 * nw + 2 * tig + e];
           lrow[nw][e] *= alpha;
           const float a = alpha * es;
           zrow[nw][e] *= a;
@@ -555,20 +567,18 @@ split_int4_kernel(const SplitParams p) {
     scores(g % kI4Stages);
     bool over = vote(kbase);
     // Between two barriers: the product of the block before, the weights of this one and the scores of the next, which
-    // do not depend on one another: in the usual case one run of instructions without a branch.
+    // do not depend on one another.
     #pragma unroll 1
     for (int blk = 0; blk < nblk - 1; ++blk, ++g) {
       copy_step(g % kI4Stages, true);
       if (over || blk == 0) {
         if (blk > 0) product((g - 1) % kI4Stages, (blk - 1) & 1);
         new_references();
-        weights(blk & 1);
-        scores((g + 1) % kI4Stages);
       } else {
         product((g - 1) % kI4Stages, (blk - 1) & 1);
-        weights(blk & 1);
-        scores((g + 1) % kI4Stages);
       }
+      weights(blk & 1);
+      scores((g + 1) % kI4Stages);
       kbase += kI4Block;
       over = vote(kbase);
     }
@@ -589,8 +599,8 @@ split_int4_kernel(const SplitParams p) {
           z += __shfl_xor_sync(0xffffffffu, z, i);
         }
         if (gid == 0) {
-          xsum[w * 16 * NQ + 8 * nw + 2 * tig + e] = l;
-          xsum[w * 16 * NQ + 8 * NQ + 8 * nw + 2 * tig + e] = z;
+          xsum[(8 * nw + 2 * tig + e) * W + w] = l;
+          xsum[(8 * NQ + 8 * nw + 2 * tig + e) * W + w] = z;
         }
       }
     cp_async_wait<kI4Stages - 2>();  // V of the last block
@@ -605,24 +615,23 @@ split_int4_kernel(const SplitParams p) {
       #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float l = 0.f, z = 0.f;
+        const float* xs = xsum + (8 * nw + 2 * tig + e) * W;
         #pragma unroll
         for (int i = 0; i < W; ++i) {
-          l += xsum[i * 16 * NQ + 8 * nw + 2 * tig + e];
-          z += xsum[i * 16 * NQ + 8 * NQ + 8 * nw + 2 * tig + e];
+          l += xs[i];
+          z += xs[8 * NQ * W + i];
         }
-        const int r = r0 + 8 * nw + 2 * tig + e;
-        if (r >= p.GT) continue;
+        if (o_rows[nw][e] < 0) continue;
         const float inv = l == 0.f ? 0.f : unref / l;
         const float lse_v = l == 0.f ? -INFINITY : (__log2f(l) - nmu[nw][e]) * LN2;
         const float v[4] = {fmaf(o[nw][0][e], 16777216.f, -z) * inv, fmaf(o[nw][0][e + 2], 1048576.f, -z) * inv,
                             fmaf(o[nw][1][e], 16777216.f, -z) * inv, fmaf(o[nw][1][e + 2], 1048576.f, -z) * inv};
-        const int t = r / p.G, g = r - t * p.G;
         if (d.slot < 0) {
-          const int64_t row = ((int64_t)d.b * p.T + t) * p.Hq + (int64_t)d.h * p.G + g;
+          const int64_t row = first_row(d) + o_rows[nw][e];
           *reinterpret_cast<uint2*>(p.out_bf16 + row * D + 32 * w + 4 * gid) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
           if (w == 0 && gid == 0) p.lse[row] = lse_v;
         } else {
-          const int64_t row = (int64_t)d.slot * p.GT + r;
+          const int64_t row = (int64_t)d.slot * p.GT + r0 + 8 * nw + 2 * tig + e;
           *reinterpret_cast<float4*>(p.part_o + row * D + 32 * w + 4 * gid) = make_float4(v[0], v[1], v[2], v[3]);
           if (w == 0 && gid == 0) p.part_lse[row] = lse_v;
         }
@@ -655,7 +664,8 @@ static cudaError_t launch_i4(const SplitParams& p, int sms, cudaStream_t st) {
 
 template <int D>
 static cudaError_t launch_i4_gt(const SplitParams& p, int sms, cudaStream_t st) {
-  return p.GT <= 8 ? launch_i4<D, 1, 4>(p, sms, st) : launch_i4<D, 2, 4>(p, sms, st);
+  constexpr int CPS = D == 64 ? 8 : 4;
+  return p.GT <= 8 ? launch_i4<D, 1, CPS>(p, sms, st) : launch_i4<D, 2, CPS>(p, sms, st);
 }
 
 bool split_int4_supported(int D, int GT) { return GT >= 1 && GT <= kMaxGT && (D == 64 || D == 128); }
