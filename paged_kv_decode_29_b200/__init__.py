@@ -528,7 +528,7 @@ def append_rope_int4(q_new: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
     holding each request's rows; k_new / v_new likewise with Hkv heads. ``k_values`` / ``v_values``:
     optional bf16 tensors like k_new (both or neither) that receive the new rows as the cache will give them
     back; ``status``: optional int32 device scalar (DECATTN_EDEVICE)."""
-    lib = load_library()
+    lib = _lib or load_library()
     shape, total = _int4_args(q_new, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, k_new, v_new, q_out,
                               k_values, v_values, status)
     kv_shape = (*q_new.shape[:-2], shape.n_kv_heads, shape.head_dim)
@@ -536,9 +536,9 @@ def append_rope_int4(q_new: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
         if t is not None and (t.shape != kv_shape or t.dtype != torch.bfloat16):
             raise ValueError("k_new, v_new and the values are bf16, q_new's rows with Hkv heads")
     q_out = _int4_result("q_out", q_out, q_new.shape, torch.bfloat16, q_new)
-    rc = lib.dec_attn_append_rope_int4(C.byref(shape), _ptr(q_new), _ptr(k_new), _ptr(v_new), _ptr(page_table),
-                                       _ptr(seq_lens), _ptr(cu_q_lens), total, rope_base, _ptr(q_out),
-                                       _ptr(k_pages), _ptr(v_pages), _ptr(kv_words), _ptr(k_values), _ptr(v_values),
+    rc = lib.dec_attn_append_rope_int4(C.byref(shape), q_new.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), page_table.data_ptr(),
+                                       seq_lens.data_ptr(), _ptr(cu_q_lens), total, rope_base, q_out.data_ptr(),
+                                       k_pages.data_ptr(), v_pages.data_ptr(), kv_words.data_ptr(), _ptr(k_values), _ptr(v_values),
                                        _ptr(status), _stream_handle(stream))
     if rc != OK:
         raise DecAttnError(rc, "dec_attn_append_rope_int4")
@@ -552,16 +552,18 @@ def run_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_w
     """dec_attn_run_int4: split + combine over an INT4 cache; returns (out bf16 [B][T][Hq][d], lse fp32
     [B][T][Hq]). q: bf16 [B][T][Hq][d]; the cache as append_rope_int4 writes it; page_table, seq_lens, the
     plan (dense or block-sparse) and the workspace as for ``run``, the workspace of a shape with KV_INT4."""
-    lib = load_library()
+    lib = _lib or load_library()
     shape, _ = _int4_args(q, k_pages, v_pages, kv_words, page_table, seq_lens, None, workspace, out, lse)
-    shape.sm_scale = sm_scale
-    out = _int4_result("out", out, q.shape, torch.bfloat16, q)
-    lse = _int4_result("lse", lse, q.shape[:-1], torch.float32, q)
+    if sm_scale:
+        shape.sm_scale = sm_scale
+    q_shape = q.shape
+    out = _int4_result("out", out, q_shape, torch.bfloat16, q)
+    lse = _int4_result("lse", lse, q_shape[:-1], torch.float32, q)
     if workspace is None:
         workspace = torch.empty(workspace_bytes(shape, pl), dtype=torch.uint8, device=q.device)
-    rc = lib.dec_attn_run_int4(C.byref(shape), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(kv_words), _ptr(page_table),
-                               _ptr(seq_lens), C.byref(pl.handle), _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse),
+    rc = lib.dec_attn_run_int4(C.byref(shape), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_words.data_ptr(), page_table.data_ptr(),
+                               seq_lens.data_ptr(), C.byref(pl.handle), workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), out.data_ptr(), lse.data_ptr(),
                                _stream_handle(stream))
     if rc != OK:
         raise DecAttnError(rc, "dec_attn_run_int4")
@@ -577,7 +579,7 @@ def prefill_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     rows. q is bf16 [B][T][Hq][128] (cu_q_lens None) or packed [total][Hq][128] with cu_q_lens int32 [B + 1] and
     ``max_q_rows`` bounding every request's rows. ``workspace``: uint8 device buffer of at least
     prefill_int4_workspace_bytes (allocated here if None)."""
-    lib = load_library()
+    lib = _lib or load_library()
     shape, total = _int4_args(q, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, workspace, out, lse, status)
     shape.sm_scale = sm_scale
     if cu_q_lens is not None:
@@ -589,9 +591,9 @@ def prefill_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
         if need < 0:
             raise DecAttnError(need, "dec_attn_prefill_int4_workspace_bytes")
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    rc = lib.dec_attn_prefill_int4(C.byref(shape), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(kv_words),
-                                   _ptr(page_table), _ptr(seq_lens), _ptr(cu_q_lens), total, _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse), _ptr(status),
+    rc = lib.dec_attn_prefill_int4(C.byref(shape), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_words.data_ptr(),
+                                   page_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_q_lens), total, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), out.data_ptr(), lse.data_ptr(), _ptr(status),
                                    _stream_handle(stream))
     if rc != OK:
         raise DecAttnError(rc, "dec_attn_prefill_int4")
