@@ -546,6 +546,42 @@ def test_prompt_then_decode_steps_over_one_cache():
             at += r
 
 
+def test_one_plan_serves_every_layer_behind_its_append():
+    """plan, then append and attention layer by layer: the attention follows the planner in the first layer and the
+    append, whose rows it has to see, in the others. Many requests: the append is the longer kernel."""
+    rng = np.random.default_rng(55)
+    B, hq, hkv, d, P, layers = 96, 8, 2, 128, 16, 3
+    have = [int(x) for x in rng.integers(1, 700, B)]
+    lens = _int32(have)
+    caches = [I4.Cache(have, Hkv=hkv, d=d, P=P, seed=56 + i) for i in range(layers)]
+    devs = [c.to_device() for c in caches]
+    rows = [_new_rows(rng, B, hq, hkv, d) for _ in range(layers)]
+    dev_rows = [[_bf16_dev(x).view(B, 1, -1, d) for x in r] for r in rows]
+    torch.cuda.synchronize()
+    for order in ("plan first", "append first"):
+        outs = []
+        for i in range(layers):
+            dev = devs[i]
+            if i == 0 and order == "plan first":
+                pl = da.plan(lens, hkv, 128, max_total_kv_tokens=sum(have))
+            qr = da.append_rope_int4(*dev_rows[i], dev["tab"], lens, dev["k"], dev["v"], dev["words"])
+            if i == 0 and order == "append first":
+                pl = da.plan(lens, hkv, 128, max_total_kv_tokens=sum(have))
+            outs.append((qr,) + da.run_int4(qr, dev["k"], dev["v"], dev["words"], dev["tab"], lens, pl))
+        assert da.read_status(pl) == da.OK
+        for i in range(layers):
+            now = I4.Cache(have, Hkv=hkv, d=d, P=P, seed=56 + i)
+            now.pools = [devs[i]["k"].cpu().numpy(), devs[i]["v"].cpu().numpy()]
+            now.words = devs[i]["words"].cpu().numpy().view(np.uint16)
+            q, out, lse = (_f64(x) for x in outs[i])
+            for b in range(B):
+                ref = I4.attend(now, b, q[b], np.array([have[b] - 1]))
+                I4.check(out[b], lse[b], ref, what=f"{order}, layer {i}, request {b}")
+            for d_, orig in zip(("k", "v"), caches[i].pools):    # as before the append, for the next order
+                devs[i][d_].copy_(torch.from_numpy(orig))
+            devs[i]["words"].copy_(torch.from_numpy(caches[i].words.view(np.int16)))
+
+
 def test_the_binding_refuses_what_it_can_see():
     cache = I4.Cache([40, 50], Hkv=2, d=128, P=16, seed=61)
     dev = cache.to_device()
