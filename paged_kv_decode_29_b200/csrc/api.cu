@@ -269,11 +269,12 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
 
 // Shared by dec_attn_prefill (cu_q null: T rows per request), dec_attn_prefill_varlen and the FP8 and
 // INT4 prefills (on their widened pools; splits > 0: the INT4 prefill's, with a bf16 output and room for the
-// parts of so many splits). check_only: every check and tensor map, no launch.
+// parts of so many splits, and `expand` launched first). check_only: every check and tensor map, no launch.
 static int prefill_enqueue(const dec_attn_shape* shape, const void* q, const void* k_pages, const void* v_pages,
                            const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_q,
                            int64_t total_rows, void* out, float* lse, int32_t* status, void* stream,
-                           bool check_only = false, int splits = 0, float* parts = nullptr) {
+                           bool check_only = false, int splits = 0, float* parts = nullptr,
+                           const WidenInt4Params* expand = nullptr) {
   const bool bf16_out = splits > 0;
   if (!shape) return DECATTN_EINVAL;
   const dec_attn_shape& s = *shape;
@@ -321,6 +322,9 @@ static int prefill_enqueue(const dec_attn_shape* shape, const void* q, const voi
   p.qk_scale_log2 = scale * 1.4426950408889634f;
   test_waits(&p.wait_ns, &p.skip_fill);
   if (check_only) return DECATTN_OK;
+  if (expand)
+    if (const cudaError_t e = launch_widen_int4(*expand, static_cast<cudaStream_t>(stream)); e != cudaSuccess)
+      return cuda_fail("INT4 prefill expansion launch", e);
   const cudaError_t e = launch_prefill(p, tmQ, tmK, tmV, tmO, tmP, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DECATTN_OK : cuda_fail("prefill kernel launch", e);
 }
@@ -379,7 +383,8 @@ static int64_t prefill_int4_scratch(const dec_attn_shape& s, int64_t* off_v, int
   const int64_t wide =
       widen_scratch_bytes(s.batch, s.max_pages_per_seq, s.n_kv_heads, s.page_size, s.head_dim, off_v, off_pt);
   const int64_t rows = (int64_t)s.batch * s.q_tokens;
-  const int n = rows > 0 ? prefill_splits(s.batch, s.q_tokens, s.n_q_heads, s.n_q_heads / s.n_kv_heads) : 1;
+  const int n = rows > 0 ? prefill_splits(s.batch, s.q_tokens, s.n_q_heads, s.n_q_heads / s.n_kv_heads,
+                                        (int64_t)s.max_pages_per_seq * s.page_size) : 1;
   if (off_parts) *off_parts = wide;
   if (splits) *splits = n;
   return wide + (n > 1 ? align_up(n * rows * s.n_q_heads * (s.head_dim + 1) * 4, 256) : 0);
@@ -417,9 +422,6 @@ static int prefill_int4_enqueue(const dec_attn_shape* shape, const void* q, cons
   wide.kv_dtype = DECATTN_KV_BF16;
   wide.num_pages = s.batch * s.max_pages_per_seq;
   const int32_t* wide_pt = reinterpret_cast<const int32_t*>(ws + off_pt);
-  const int rc = prefill_enqueue(&wide, q, ws, ws + off_v, wide_pt, seq_lens, cu_q, total_rows, out, lse, status,
-                                 stream, /*check_only=*/true, splits, parts);
-  if (rc != DECATTN_OK) return rc;
   WidenInt4Params w;
   w.k_codes = static_cast<const uint8_t*>(k_pages);
   w.v_codes = static_cast<const uint8_t*>(v_pages);
@@ -432,10 +434,8 @@ static int prefill_int4_enqueue(const dec_attn_shape* shape, const void* q, cons
   w.status = status;
   w.B = s.batch; w.Hkv = s.n_kv_heads; w.P = s.page_size;
   w.num_pages = s.num_pages; w.mpps = s.max_pages_per_seq;
-  const cudaError_t e = launch_widen_int4(w, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail("INT4 prefill expansion launch", e);
   return prefill_enqueue(&wide, q, ws, ws + off_v, wide_pt, seq_lens, cu_q, total_rows, out, lse, status, stream,
-                         /*check_only=*/false, splits, parts);
+                         /*check_only=*/false, splits, parts, &w);
 }
 
 }  // namespace decattn

@@ -522,7 +522,7 @@ cudaError_t launch_combine(const CombineParams& p, int device, cudaStream_t st);
 cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                            const CUtensorMap& tmV, const CUtensorMap& tmO, const CUtensorMap& tmP,
                            cudaStream_t st);                      // prefill.cu
-int prefill_splits(int B, int T, int Hq, int G);                  // prefill.cu
+int prefill_splits(int B, int T, int Hq, int G, int64_t max_keys);  // prefill.cu
 // bytes of the widened pool (K, then V at *off_v, then the page table at *off_pt)   prefill_fp8.cu
 int64_t widen_scratch_bytes(int B, int mpps, int Hkv, int P, int D, int64_t* off_v, int64_t* off_pt);
 cudaError_t launch_widen_kv(const WidenParams& p, cudaStream_t st);  // prefill_fp8.cu

@@ -641,13 +641,16 @@ __global__ void __launch_bounds__(kPfcThreads) prefill_combine_kernel(const Pref
 }
 
 // Parts that the keys are split into at most: as many as bring the grid to four CTAs per multiprocessor of a B200
-// (they differ in length: the heaviest come first, short ones fill up), 16 at most. On 5 ragged chunks (a grid
-// of 200): 137 us in one part, 104 in three, 111 in eight (more parts to write and merge).
-int prefill_splits(int B, int T, int Hq, int G) {
+// (they differ in length: the heaviest come first, short ones fill up), 16 at most, and no more than a request
+// with max_keys keys can have. On 5 ragged chunks (a grid of 200): 137 us in one part, 104 in three, 111 in eight
+// (more parts to write and merge).
+int prefill_splits(int B, int T, int Hq, int G, int64_t max_keys) {
   const int64_t grid = pf_grid(B, T, Hq, G);
   if (grid <= 0) return 1;
-  const int64_t n = (4 * 148 + grid - 1) / grid;
-  return (int)(n > 16 ? 16 : n);
+  int64_t n = (4 * 148 + grid - 1) / grid;
+  if (n > 16) n = 16;
+  const int64_t most = (max_keys + 4 * kPfN - 1) / (4 * kPfN);  // prefill_part_blocks: four key blocks at least
+  return (int)(n < most ? n : most < 1 ? 1 : most);
 }
 
 cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
