@@ -485,10 +485,11 @@ DECATTN_API int dec_attn_append_rope_int4(const dec_attn_shape *shape, const voi
 /* dec_attn_run over an INT4 cache: split + combine for shape->kv_dtype DECATTN_KV_INT4.
  *   kv_words  device uint16 [2][num_pages][Hkv][P], 16-byte aligned (codes too);
  *   out       bf16 [B][T][Hq][d], 16-byte aligned, rounded once from fp32; lse fp32 [B][T][Hq].
- * Other arguments, shapes, errors and stream rules as dec_attn_run; dense and block-sparse plans. The scores
- * are exact products of q and the cache's values, summed in fp32; a weight times a V scale is rounded to f16
- * (2^-11 half a step, below bf16's 2^-9) for the second product. Slots behind a request's last key, their
- * words among them, may hold anything. */
+ * Other arguments, shapes, errors and stream rules as dec_attn_run; dense and block-sparse plans (this kernel has no
+ * pipeline wait, so it never reports DECATTN_ETIMEOUT). Scores are fp32 sums of exact products of q and the
+ * codes; a weight times a V scale is rounded to f16 (2^-11 half a step, where bf16's is 2^-8) for the second
+ * product. Slots behind a request's last key, their words among them, may hold anything. A query row that sees a NaN
+ * row of the cache gets NaN in out (in lse too, if the row is one of K); no other row does. */
 DECATTN_API int dec_attn_run_int4(const dec_attn_shape *shape, const void *q, const void *k_pages,
                                   const void *v_pages, const void *kv_words, const int32_t *page_table,
                                   const int32_t *seq_lens, const dec_attn_plan_t *plan, void *workspace,

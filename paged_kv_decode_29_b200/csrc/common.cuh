@@ -209,10 +209,10 @@ struct PrefillParams {
 };
 
 // Key blocks of 128 that one CTA of a split prefill takes of a request with Lb keys; a row block that sees n
-// key blocks has ceil(n / that) parts. Short requests are split less: a part has four blocks at least.
+// key blocks has ceil(n / that) parts. Short requests are split less: a part has two blocks at least.
 __host__ __device__ inline int prefill_part_blocks(int Lb, int splits) {
   const int n = (Lb + 127) / 128, per = (n + splits - 1) / splits;
-  return per < 4 ? 4 : per;
+  return per < 2 ? 2 : per;
 }
 
 // FP8 prefill: the E4M3 pages each request uses, widened to a bf16 scratch pool (prefill_fp8.cu).

@@ -588,6 +588,7 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
 // The parts of a split prefill into the output: a warp takes one (packed row, q head), lane l head dims
 // 4 l .. 4 l + 3. Rows of one part were written by their CTA; rows behind the last request are left alone.
 constexpr int kPfcThreads = 256;
+constexpr int kPfMaxParts = 32;  // a lane of the combine each
 
 __global__ void __launch_bounds__(kPfcThreads) prefill_combine_kernel(const PrefillParams p) {
   griddep_wait();
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(kPfcThreads) prefill_combine_kernel(const Pref
   const int parts = (nkb + per - 1) / per;
   if (parts <= 1) return;
   const int64_t stride = p.total_rows * p.Hq;
-  const float my = lane < parts ? p.part_lse[lane * stride + item] : -INFINITY;  // at most 16 parts
+  const float my = lane < parts ? p.part_lse[lane * stride + item] : -INFINITY;  // at most kPfMaxParts parts
   float M = my;
   #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -640,16 +641,17 @@ __global__ void __launch_bounds__(kPfcThreads) prefill_combine_kernel(const Pref
   if (lane == 0) p.lse[item] = W == 0.f ? -INFINITY : M + logf(W);
 }
 
-// Parts that the keys are split into at most: as many as bring the grid to four CTAs per multiprocessor of a B200
-// (they differ in length: the heaviest come first, short ones fill up), 16 at most, and no more than a request
-// with max_keys keys can have. On 5 ragged chunks (a grid of 200): 137 us in one part, 104 in three, 111 in eight
-// (more parts to write and merge).
+// Parts that the keys are split into at most, and no more than a request with max_keys keys can have. A small grid
+// becomes one wave of a B200's 148 multiprocessors (a CTA fills one, and its start and end cost as much as four key
+// blocks); a larger one up to four waves, whose parts differ in length (the heaviest come first, short ones
+// fill up), in four parts at most. 5 ragged chunks (a grid of 200): 137 us in one part, 104 in three, 111 in
+// eight. 106 rows over 9982 keys (a grid of 24): 40.9 us in 10 parts (two waves), 32.7 in six.
 int prefill_splits(int B, int T, int Hq, int G, int64_t max_keys) {
   const int64_t grid = pf_grid(B, T, Hq, G);
   if (grid <= 0) return 1;
-  int64_t n = (4 * 148 + grid - 1) / grid;
-  if (n > 16) n = 16;
-  const int64_t most = (max_keys + 4 * kPfN - 1) / (4 * kPfN);  // prefill_part_blocks: four key blocks at least
+  int64_t n = grid <= 74 ? 148 / grid : (4 * 148 + grid - 1) / grid;
+  if (n > (grid <= 74 ? kPfMaxParts : 4)) n = grid <= 74 ? kPfMaxParts : 4;
+  const int64_t most = (max_keys + 2 * kPfN - 1) / (2 * kPfN);  // prefill_part_blocks: two key blocks at least
   return (int)(n < most ? n : most < 1 ? 1 : most);
 }
 

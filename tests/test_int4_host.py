@@ -172,7 +172,7 @@ def test_prefill_host_checks(lib):
     assert need == pools                                             # 128 keys at most: one part
     long = _shape(q_tokens=300, max_pages_per_seq=1000)
     wide = 2 * (B * 1000 * Hkv * P * 128 * 2) + -(-(B * 1000 * 4) // 256) * 256
-    assert lib.dec_attn_prefill_int4_workspace_bytes(C.byref(long)) == wide + 16 * (B * 300 * 8 * 129 * 4)  # 24 CTAs
+    assert lib.dec_attn_prefill_int4_workspace_bytes(C.byref(long)) == wide + 6 * (B * 300 * 8 * 129 * 4)  # 24 CTAs: 6 parts
     many = _shape(q_tokens=300, n_q_heads=592)                       # a grid that fills the GPU: no parts
     assert lib.dec_attn_prefill_int4_workspace_bytes(C.byref(many)) == pools
     assert lib.dec_attn_prefill_int4_workspace_bytes(C.byref(_shape(q_tokens=0))) == da.EINVAL
