@@ -489,7 +489,7 @@ DECATTN_API int dec_attn_append_rope_int4(const dec_attn_shape *shape, const voi
  * pipeline wait, so it never reports DECATTN_ETIMEOUT). Scores are fp32 sums of exact products of q and the
  * codes; a weight times a V scale is rounded to f16 (2^-11 half a step, where bf16's is 2^-8) for the second
  * product. Slots behind a request's last key, their words among them, may hold anything. A query row that sees a NaN
- * row of the cache gets NaN in out (in lse too, if the row is one of K); no other row does. */
+ * row of K gets NaN in out and lse, one that sees a NaN row of V in out; no other row does. */
 DECATTN_API int dec_attn_run_int4(const dec_attn_shape *shape, const void *q, const void *k_pages,
                                   const void *v_pages, const void *kv_words, const int32_t *page_table,
                                   const int32_t *seq_lens, const dec_attn_plan_t *plan, void *workspace,
@@ -503,12 +503,11 @@ DECATTN_API int64_t dec_attn_prefill_int4_workspace_bytes(const dec_attn_shape *
  * 16): the pages of the requests are expanded into `workspace` as a bf16 pool (exact) and the bf16 prefill
  * kernel runs on it. Arguments as dec_attn_prefill_fp8 with kv_words (16-byte aligned, like codes and
  * workspace) in place of the scales, and
- *   total_q_rows  at most batch * q_tokens (DECATTN_EINVAL otherwise): q_tokens bounds every request's rows;
  *   out  bf16 [rows][Hq][128], 16-byte aligned, rounded once from fp32; lse fp32 [rows][Hq].
  * Where the rows are few, the keys of a request are split over several CTAs and their fp32 parts merged (third
- * launch). Weights are rounded to bf16 for the second product, as dec_attn_prefill rounds them. A row that sees a NaN
- * row of the cache gets NaN in out and lse; no other row does. Rows from cu_q_lens[batch] to total_q_rows are
- * left as they were. */
+ * launch). Weights are rounded to bf16 for the second product, as dec_attn_prefill rounds them. A query row that
+ * sees a NaN row of the cache gets NaN in out and lse; no other row does. Rows from cu_q_lens[batch] to
+ * total_q_rows are left as they were. */
 DECATTN_API int dec_attn_prefill_int4(const dec_attn_shape *shape, const void *q, const void *k_pages,
                                       const void *v_pages, const void *kv_words, const int32_t *page_table,
                                       const int32_t *seq_lens, const int32_t *cu_q_lens, int64_t total_q_rows,

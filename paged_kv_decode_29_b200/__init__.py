@@ -464,7 +464,8 @@ _INT4_PLACE = "every tensor must be contiguous and on the current CUDA device"
 
 
 def _int4_args(rows: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_words: torch.Tensor,
-               page_table: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch.Tensor | None, *others):
+               page_table: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch.Tensor | None, *others,
+               status: torch.Tensor | None = None):
     """The shape of a call over an INT4 cache and its total rows, after the checks that only the tensors allow.
     ``rows`` is q: [B][T][Hq][d], or packed [total][Hq][d] with cu_q_lens (q_tokens is 1 then); ``others`` are its
     remaining tensors (None: not given). Kernels run on the current device, so every tensor has to be there."""
@@ -503,6 +504,8 @@ def _int4_args(rows: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     for t in others if cu_q_lens is None else (cu_q_lens, *others):
         if t is not None and (t.get_device() != dev or not t.is_contiguous()):
             raise ValueError(_INT4_PLACE)
+    if status is not None and (status.dtype != torch.int32 or status.numel() != 1 or status.get_device() != dev):
+        raise ValueError("status is an int32 scalar on the current CUDA device")
     return ShapeT(B, q_shape[-2], pool_shape[1], q_shape[-1], T, pool_shape[2], pool_shape[0], mpps, KV_INT4, 0.0), total
 
 
@@ -530,7 +533,7 @@ def append_rope_int4(q_new: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
     back; ``status``: optional int32 device scalar (DECATTN_EDEVICE)."""
     lib = _lib or load_library()
     shape, total = _int4_args(q_new, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, k_new, v_new, q_out,
-                              k_values, v_values, status)
+                              k_values, v_values, status=status)
     kv_shape = (*q_new.shape[:-2], shape.n_kv_heads, shape.head_dim)
     for t in (k_new, v_new, k_values, v_values):
         if t is not None and (t.shape != kv_shape or t.dtype != torch.bfloat16):
@@ -580,7 +583,7 @@ def prefill_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     ``max_q_rows`` bounding every request's rows. ``workspace``: uint8 device buffer of at least
     prefill_int4_workspace_bytes (allocated here if None)."""
     lib = _lib or load_library()
-    shape, total = _int4_args(q, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, workspace, out, lse, status)
+    shape, total = _int4_args(q, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, workspace, out, lse, status=status)
     shape.sm_scale = sm_scale
     if cu_q_lens is not None:
         shape.q_tokens = int(max_q_rows)

@@ -404,7 +404,8 @@ static int prefill_int4_enqueue(const dec_attn_shape* shape, const void* q, cons
   if (s.kv_dtype != DECATTN_KV_INT4 || s.head_dim != 128 || s.page_size % 16 != 0) return DECATTN_ENOTSUP;
   if (s.batch > 65535 || s.n_q_heads > 65535 || (int64_t)s.batch * s.q_tokens * s.n_q_heads >= (1ll << 31))
     return DECATTN_ENOTSUP;
-  if (total_rows > (int64_t)s.batch * s.q_tokens) return DECATTN_EINVAL;  // q_tokens bounds every request's rows
+  // q_tokens bounds every request's rows: what lies behind (a padded batch) is no request's
+  if (total_rows > (int64_t)s.batch * s.q_tokens) total_rows = (int64_t)s.batch * s.q_tokens;
   if ((int64_t)s.batch * s.max_pages_per_seq >= (1ll << 31) || s.n_kv_heads > 65535) return DECATTN_ENOTSUP;
   if (s.batch == 0 || total_rows == 0) return DECATTN_OK;
   if (!k_pages || !v_pages || !kv_words || !page_table || !seq_lens || !workspace) return DECATTN_EINVAL;

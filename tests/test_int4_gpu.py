@@ -237,7 +237,7 @@ def test_decode_matches_64_bit_attention(hq, hkv, d, T, P, lens, tile):
     _check_decode(cache, q, T, out, lse)
 
 
-@pytest.mark.parametrize("n_bins", [1, 3, 592])
+@pytest.mark.parametrize("n_bins", [1, 3, 592, 1500])
 def test_decode_with_other_bins_and_scale(n_bins):
     cache = I4.Cache([700, 33, 1200], Hkv=2, d=128, P=16, seed=11)
     q = I4.bf16(np.random.default_rng(12).standard_normal((3, 1, 8, 128)))
@@ -436,6 +436,7 @@ def test_prefill_uniform_matches_64_bit_attention(hq, hkv, P, lens, T):
     ([300, 40, 129], [1, 40, 129], 0),
     ([500, 20, 0, 64], [160, 0, 3, 64], 37),  # no rows; rows without a key; a padded batch
     ([5000, 700, 130], [257, 130, 1], 3),     # keys split over CTAs: many parts, few, one
+    ([2000], [5], 300),                       # far more padding than rows
 ])
 def test_prefill_packed_matches_64_bit_attention(lens, rows, pad):
     cache = I4.Cache(lens, Hkv=2, d=128, P=16, seed=41 + pad)
@@ -464,8 +465,10 @@ def test_prefill_nan_rows_bad_pages_and_offsets():
         dev["tab"][0, 3] = bad
         out, _ = _prefill(cache, q, rows, uniform=False, dev=dev, expect=da.EDEVICE)
         assert np.array_equal(out[100:], ref[100:])
-    with pytest.raises(AssertionError):                      # offsets outside the rows: that request is not written
-        _prefill(cache, q, rows, uniform=False, cu=[0, 100, 400], max_rows=300)
+    for cu, max_rows in (([0, 100, 400], 300), ([0, 100, 250], 149), ([0, 240, 390], 150), ([-1, 100, 250], 150)):
+        out, _ = _prefill(cache, q, rows, uniform=False, cu=cu, max_rows=max_rows, expect=da.EDEVICE)
+        if cu[1] == 100 and cu[0] == 0:                      # offsets outside the rows: only that request is not written
+            assert np.array_equal(out[:100], ref[:100]) and np.all(out[100:] == 5.0)
 
 
 def test_prefill_is_the_bf16_prefill_over_the_caches_values():
