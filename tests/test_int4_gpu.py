@@ -471,6 +471,22 @@ def test_prefill_nan_rows_bad_pages_and_offsets():
             assert np.array_equal(out[:100], ref[:100]) and np.all(out[100:] == 5.0)
 
 
+def test_prefill_nan_rows_in_split_keys():
+    cache = I4.Cache([3000], Hkv=2, d=128, P=16, seed=62)
+    q = I4.bf16(np.random.default_rng(63).standard_normal((100, 4, 128)))
+    ref, ref_l = _prefill(cache, q, [100], uniform=True)
+    for which, pos in ((0, 100), (1, 100), (0, 2950), (1, 2950)):
+        pid, slot = cache.table[0, pos // 16], pos % 16
+        saved = cache.words[which, pid, 0, slot]
+        cache.words[which, pid, 0, slot] = 0x7FC0
+        out, lse = _prefill(cache, q, [100], uniform=True)
+        cache.words[which, pid, 0, slot] = saved
+        sees = np.zeros((100, 4), dtype=bool)
+        sees[max(pos - 2900, 0):, :2] = True
+        assert np.isnan(out[sees]).all() and np.isnan(lse[sees]).all(), (which, pos)
+        assert np.array_equal(out[~sees], ref[~sees]) and np.array_equal(lse[~sees], ref_l[~sees])
+
+
 def test_prefill_is_the_bf16_prefill_over_the_caches_values():
     """Where the keys are not split: the same kernel over the same numbers, so equal to dec_attn_prefill over the
     values, rounded to bf16."""
@@ -583,6 +599,53 @@ def test_one_plan_serves_every_layer_behind_its_append():
             for d_, orig in zip(("k", "v"), caches[i].pools):    # as before the append, for the next order
                 devs[i][d_].copy_(torch.from_numpy(orig))
             devs[i]["words"].copy_(torch.from_numpy(caches[i].words.view(np.int16)))
+
+
+def test_pools_beyond_32_bit_offsets():
+    """The same cache with its pages at the end of pools of 5 GB: appended to, decoded and prefilled alike."""
+    cache = I4.Cache([700, 300], Hkv=8, d=128, P=64, seed=57)
+    small = cache.to_device()
+    shift = 160_000                                          # rows from 82 million, bytes from 5.2 billion on
+    n = shift + cache.num_pages
+    large = dict(k=torch.zeros((n, 8, 64, 64), dtype=torch.uint8, device="cuda"),
+                 v=torch.zeros((n, 8, 64, 64), dtype=torch.uint8, device="cuda"),
+                 words=torch.zeros((2, n, 8, 64), dtype=torch.uint16, device="cuda").view(torch.int16),
+                 tab=torch.where(small["tab"] >= 0, small["tab"] + shift, small["tab"]), lens=small["lens"])
+    large["k"][shift:], large["v"][shift:], large["words"][:, shift:] = small["k"], small["v"], small["words"]
+    rng = np.random.default_rng(58)
+    rows = [_bf16_dev(x).view(2, 3, -1, 128) for x in _new_rows(rng, 6, 16, 8, 128)]
+    res = []
+    for dev in (small, large):
+        st = torch.zeros((), dtype=torch.int32, device="cuda")
+        q = da.append_rope_int4(*rows, dev["tab"], dev["lens"], dev["k"], dev["v"], dev["words"], status=st)
+        pl = da.plan(dev["lens"], 8, 256, max_total_kv_tokens=1000)
+        res.append((q,) + da.run_int4(q, dev["k"], dev["v"], dev["words"].view(torch.uint16), dev["tab"], dev["lens"], pl)
+                   + da.prefill_int4(q, dev["k"], dev["v"], dev["words"], dev["tab"], dev["lens"], status=st))
+        assert da.read_status(pl) == da.OK and int(st) == da.OK
+    for x, y in zip(*res):
+        assert torch.equal(x, y)
+    assert torch.equal(small["k"], large["k"][shift:]) and torch.equal(small["v"], large["v"][shift:])
+    assert torch.equal(small["words"], large["words"][:, shift:])
+    assert not large["k"][:shift].any() and not large["v"][:shift].any()
+
+
+def test_two_streams_at_once():
+    caches = [I4.Cache([4000, 900, 64], Hkv=4, d=128, P=16, seed=64 + i) for i in range(2)]
+    qs = [I4.bf16(np.random.default_rng(66 + i).standard_normal((3, 2, 16, 128))) for i in range(2)]
+    ref = [_decode(c, q, 2, tile=128) for c, q in zip(caches, qs)]
+    devs, dq, streams = [c.to_device() for c in caches], [_bf16_dev(q) for q in qs], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                d = devs[i]
+                pl = da.plan(d["lens"], 4, 128, max_total_kv_tokens=4964)
+                got[i].append((pl,) + da.run_int4(dq[i], d["k"], d["v"], d["words"], d["tab"], d["lens"], pl))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for _, out, lse in got[i]:
+            assert np.array_equal(_f64(out), ref[i][0]) and np.array_equal(_f64(lse), ref[i][1])
 
 
 def test_the_binding_refuses_what_it_can_see():
