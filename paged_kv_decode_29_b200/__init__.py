@@ -146,9 +146,14 @@ def last_error() -> str:
     return buf.value.decode(errors="replace")
 
 
+def _raw_stream(device: int) -> int | None:
+    """The handle of the device's current stream (a torch.cuda.Stream object would take 3 us to make)."""
+    return torch._C._cuda_getCurrentRawStream(device) or None
+
+
 def _stream_handle(stream) -> int | None:
-    if stream is None:  # the raw handle: a torch.cuda.Stream object would take 3 us to make
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+    if stream is None:
+        return _raw_stream(torch.cuda.current_device())
     h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     return h or None
 
@@ -460,40 +465,43 @@ def prefill_fp8_workspace_bytes(q_shape, k_pages: torch.Tensor, page_table: torc
     return n
 
 
+_BF16, _I32, _U8, _I16, _U16 = torch.bfloat16, torch.int32, torch.uint8, torch.int16, torch.uint16
 _INT4_PLACE = "every tensor must be contiguous and on the current CUDA device"
 
 
 def _int4_args(rows: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_words: torch.Tensor,
                page_table: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch.Tensor | None, *others,
                status: torch.Tensor | None = None):
-    """The shape of a call over an INT4 cache and its total rows, after the checks that only the tensors allow.
+    """The shape of a call over an INT4 cache, its total rows and device, after the checks that only the tensors allow.
     ``rows`` is q: [B][T][Hq][d], or packed [total][Hq][d] with cu_q_lens (q_tokens is 1 then); ``others`` are its
     remaining tensors (None: not given). Kernels run on the current device, so every tensor has to be there."""
-    q_shape, pool_shape = rows.shape, k_pages.shape
     B, mpps = page_table.shape
     if cu_q_lens is None:
-        if len(q_shape) != 4 or q_shape[0] != B:
+        if rows.dim() != 4:
             raise ValueError("q is [B][T][Hq][d], or packed [total][Hq][d] with cu_q_lens")
-        T = q_shape[1]
+        n, T, Hq, d = rows.shape
+        if n != B:
+            raise ValueError("q and page_table hold different numbers of requests")
         total = B * T
     else:
-        if len(q_shape) != 3 or cu_q_lens.shape != (B + 1,):
+        if rows.dim() != 3 or cu_q_lens.shape != (B + 1,):
             raise ValueError("packed q is [total][Hq][d] with cu_q_lens [B + 1]")
-        if cu_q_lens.dtype != torch.int32:
+        if cu_q_lens.dtype != _I32:
             raise TypeError("cu_q_lens must be int32")
-        T, total = 1, q_shape[0]
-    if seq_lens.shape != (B,):
+        total, Hq, d = rows.shape
+        T = 1
+    if seq_lens.dim() != 1 or seq_lens.numel() != B:
         raise ValueError("page_table is [B][max_pages_per_seq] and seq_lens [B]")
-    if rows.dtype != torch.bfloat16:
+    if rows.dtype != _BF16:
         raise TypeError("q must be bf16")
-    if page_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+    if page_table.dtype != _I32 or seq_lens.dtype != _I32:
         raise TypeError("page_table and seq_lens must be int32")
-    if k_pages.dtype != torch.uint8 or v_pages.dtype != torch.uint8:
+    if k_pages.dtype != _U8 or v_pages.dtype != _U8:
         raise TypeError("INT4 pools are uint8, two codes to a byte")
-    if kv_words.dtype != torch.int16 and kv_words.dtype != torch.uint16:
+    if kv_words.dtype != _I16 and kv_words.dtype != _U16:
         raise TypeError("kv_words are 16-bit words (int16 or uint16)")
-    if (len(pool_shape) != 4 or 2 * pool_shape[3] != q_shape[-1] or v_pages.shape != pool_shape
-            or kv_words.shape != (2,) + pool_shape[:3]):
+    num_pages, Hkv, P, half = pools = k_pages.shape
+    if 2 * half != d or v_pages.shape != pools or kv_words.shape != (2, num_pages, Hkv, P):
         raise ValueError("an INT4 cache is k_pages / v_pages [num_pages][Hkv][P][d / 2], kv_words [2][num_pages][Hkv][P]")
     dev = torch.cuda.current_device()
     if not (rows.get_device() == k_pages.get_device() == v_pages.get_device() == kv_words.get_device() == dev
@@ -504,9 +512,9 @@ def _int4_args(rows: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     for t in others if cu_q_lens is None else (cu_q_lens, *others):
         if t is not None and (t.get_device() != dev or not t.is_contiguous()):
             raise ValueError(_INT4_PLACE)
-    if status is not None and (status.dtype != torch.int32 or status.numel() != 1 or status.get_device() != dev):
+    if status is not None and (status.dtype != _I32 or status.numel() != 1 or status.get_device() != dev):
         raise ValueError("status is an int32 scalar on the current CUDA device")
-    return ShapeT(B, q_shape[-2], pool_shape[1], q_shape[-1], T, pool_shape[2], pool_shape[0], mpps, KV_INT4, 0.0), total
+    return ShapeT(B, Hq, Hkv, d, T, P, num_pages, mpps, KV_INT4, 0.0), total, dev
 
 
 def _int4_result(name: str, t: torch.Tensor | None, shape, dtype, like: torch.Tensor) -> torch.Tensor:
@@ -532,17 +540,17 @@ def append_rope_int4(q_new: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
     optional bf16 tensors like k_new (both or neither) that receive the new rows as the cache will give them
     back; ``status``: optional int32 device scalar (DECATTN_EDEVICE)."""
     lib = _lib or load_library()
-    shape, total = _int4_args(q_new, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, k_new, v_new, q_out,
+    shape, total, dev = _int4_args(q_new, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, k_new, v_new, q_out,
                               k_values, v_values, status=status)
     kv_shape = (*q_new.shape[:-2], shape.n_kv_heads, shape.head_dim)
     for t in (k_new, v_new, k_values, v_values):
-        if t is not None and (t.shape != kv_shape or t.dtype != torch.bfloat16):
+        if t is not None and (t.dtype != _BF16 or t.shape != kv_shape):
             raise ValueError("k_new, v_new and the values are bf16, q_new's rows with Hkv heads")
-    q_out = _int4_result("q_out", q_out, q_new.shape, torch.bfloat16, q_new)
-    rc = lib.dec_attn_append_rope_int4(C.byref(shape), q_new.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), page_table.data_ptr(),
-                                       seq_lens.data_ptr(), _ptr(cu_q_lens), total, rope_base, q_out.data_ptr(),
-                                       k_pages.data_ptr(), v_pages.data_ptr(), kv_words.data_ptr(), _ptr(k_values), _ptr(v_values),
-                                       _ptr(status), _stream_handle(stream))
+    q_out = _int4_result("q_out", q_out, q_new.shape, _BF16, q_new)
+    rc = lib.dec_attn_append_rope_int4(C.byref(shape), q_new.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+                                       page_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_q_lens), total, rope_base,
+                                       q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_words.data_ptr(),
+                                       _ptr(k_values), _ptr(v_values), _ptr(status), _raw_stream(dev) if stream is None else _stream_handle(stream))
     if rc != OK:
         raise DecAttnError(rc, "dec_attn_append_rope_int4")
     return q_out
@@ -556,18 +564,18 @@ def run_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_w
     [B][T][Hq]). q: bf16 [B][T][Hq][d]; the cache as append_rope_int4 writes it; page_table, seq_lens, the
     plan (dense or block-sparse) and the workspace as for ``run``, the workspace of a shape with KV_INT4."""
     lib = _lib or load_library()
-    shape, _ = _int4_args(q, k_pages, v_pages, kv_words, page_table, seq_lens, None, workspace, out, lse)
+    shape, _, dev = _int4_args(q, k_pages, v_pages, kv_words, page_table, seq_lens, None, workspace, out, lse)
     if sm_scale:
         shape.sm_scale = sm_scale
     q_shape = q.shape
-    out = _int4_result("out", out, q_shape, torch.bfloat16, q)
+    out = _int4_result("out", out, q_shape, _BF16, q)
     lse = _int4_result("lse", lse, q_shape[:-1], torch.float32, q)
     if workspace is None:
         workspace = torch.empty(workspace_bytes(shape, pl), dtype=torch.uint8, device=q.device)
-    rc = lib.dec_attn_run_int4(C.byref(shape), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_words.data_ptr(), page_table.data_ptr(),
-                               seq_lens.data_ptr(), C.byref(pl.handle), workspace.data_ptr(),
+    rc = lib.dec_attn_run_int4(C.byref(shape), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_words.data_ptr(),
+                               page_table.data_ptr(), seq_lens.data_ptr(), C.byref(pl.handle), workspace.data_ptr(),
                                workspace.numel() * workspace.element_size(), out.data_ptr(), lse.data_ptr(),
-                               _stream_handle(stream))
+                               _raw_stream(dev) if stream is None else _stream_handle(stream))
     if rc != OK:
         raise DecAttnError(rc, "dec_attn_run_int4")
     return out, lse
@@ -583,11 +591,11 @@ def prefill_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     ``max_q_rows`` bounding every request's rows. ``workspace``: uint8 device buffer of at least
     prefill_int4_workspace_bytes (allocated here if None)."""
     lib = _lib or load_library()
-    shape, total = _int4_args(q, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, workspace, out, lse, status=status)
+    shape, total, dev = _int4_args(q, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, workspace, out, lse, status=status)
     shape.sm_scale = sm_scale
     if cu_q_lens is not None:
         shape.q_tokens = int(max_q_rows)
-    out = _int4_result("out", out, q.shape, torch.bfloat16, q)
+    out = _int4_result("out", out, q.shape, _BF16, q)
     lse = _int4_result("lse", lse, q.shape[:-1], torch.float32, q)
     if workspace is None:
         need = lib.dec_attn_prefill_int4_workspace_bytes(C.byref(shape))
@@ -597,7 +605,7 @@ def prefill_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     rc = lib.dec_attn_prefill_int4(C.byref(shape), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_words.data_ptr(),
                                    page_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_q_lens), total, workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), out.data_ptr(), lse.data_ptr(), _ptr(status),
-                                   _stream_handle(stream))
+                                   _raw_stream(dev) if stream is None else _stream_handle(stream))
     if rc != OK:
         raise DecAttnError(rc, "dec_attn_prefill_int4")
     return out, lse
