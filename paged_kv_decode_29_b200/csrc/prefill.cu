@@ -179,10 +179,23 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
   const int ny = head_pair ? p.Hq / 2 : p.Hq;
   const int nsteps = head_pair ? pf_tiles_per_head(p.T) : (pf_tiles_per_head(p.T) + 1) / 2;
   const int nsplit = BF16OUT ? p.splits : 1;
-  const int step = nsteps - 1 - (int)blockIdx.x / (p.B * ny * nsplit);
-  const int split = (int)blockIdx.x / (p.B * ny) % nsplit;
-  const int rem = (int)blockIdx.x % (p.B * ny);
-  const int b = rem / ny, y = rem % ny;
+  int step = nsteps - 1 - (int)blockIdx.x / (p.B * ny * nsplit);
+  int split = (int)blockIdx.x / (p.B * ny) % nsplit;
+  int b = (int)blockIdx.x % (p.B * ny) / ny;
+  const int y = (int)blockIdx.x % ny;
+  if (BF16OUT && nsplit > 1 && p.B <= 32) {
+    // a small grid of requests of unequal length: the longest request's CTAs first, all of its parts
+    const int i = (int)blockIdx.x / ny;
+    step = nsteps - 1 - i / nsplit % nsteps;
+    split = i % nsplit;
+    const int len = lane < p.B ? p.seq_lens[lane] : 0;
+    int before = 0;  // requests ahead of request `lane`
+    for (int j = 0; j < p.B; ++j) {
+      const int lj = __shfl_sync(0xffffffffu, len, j);
+      before += lj > len || (lj == len && j < lane) ? 1 : 0;
+    }
+    b = __ffs(__ballot_sync(0xffffffffu, lane < p.B && before == i / (nsplit * nsteps))) - 1;
+  }
   const int Lb = p.seq_lens[b];
   // the request's query rows: Tb of them from packed row qoff on
   int Tb = p.T;
