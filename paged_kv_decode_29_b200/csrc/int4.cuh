@@ -27,16 +27,20 @@ __device__ __forceinline__ void int4_to_f16_codes(uint32_t x, uint32_t (&o)[4]) 
   o[3] = y & 0x00f000f0u;
 }
 
-// The eight elements of a word of codes, as bf16 pairs in order (element 2 i in the low half of pair i).
+// The eight elements of a word of codes, as bf16 pairs in order (element 2 i in the low half of pair i). A code under
+// 128's bf16 pattern (step 1) is 128 + c; less 128 + z it is c - z, and that times s has at most eight significant
+// bits: both operations are exact. No conversions: fp32 with one a code took 2 us more for 90 MB of bf16.
 __device__ __forceinline__ uint4 int4_to_bf16(uint32_t x, uint32_t word) {
-  const float s = int4_scale(word);
-  const int z = (int)(word & 15u);
+  const __nv_bfloat162 s = __bfloat162bfloat162(__ushort_as_bfloat16((unsigned short)(word & 0xfff0u)));
+  const __nv_bfloat162 z = __bfloat162bfloat162(__ushort_as_bfloat16((unsigned short)(0x4300u | (word & 15u))));
+  const uint32_t y = x >> 4;
   uint32_t o[4];
   #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = __float_as_uint(s * (float)((int)((x >> (8 * i)) & 15u) - z));      // exact: 8
-    const uint32_t hi = __float_as_uint(s * (float)((int)((x >> (8 * i + 4)) & 15u) - z));  // significant bits
-    o[i] = (lo >> 16) | (hi & 0xffff0000u);
+    // byte i of x under the low half, of x >> 4 under the high half; the mask keeps the codes alone
+    const uint32_t c = (__byte_perm(x, y, (uint32_t)(i | (4 + i) << 8)) & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 v = __hmul2(__hsub2(reinterpret_cast<const __nv_bfloat162&>(c), z), s);
+    o[i] = reinterpret_cast<const uint32_t&>(v);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }

@@ -20,6 +20,7 @@ namespace decattn {
 
 constexpr int kWiThreads = 128;
 constexpr int kWiD = 128;
+constexpr int kWiBatch = 4;  // 16-byte outputs of K and of V that a thread has in flight
 
 // CTA (w, h): scratch page w = b * mpps + i (page i of request b), KV head h, K and V. A thread takes
 // 8 codes (4 bytes) of a row at a time and writes 16 bytes, so a warp reads two rows' codes (128 bytes)
@@ -51,17 +52,27 @@ __global__ void __launch_bounds__(kWiThreads) widen_int4_kernel(const WidenInt4P
   uint4* ko = reinterpret_cast<uint4*>(p.k_out) + dst * (kWiD / 8);
   uint4* vo = reinterpret_cast<uint4*>(p.v_out) + dst * (kWiD / 8);
   const int n = (rows + 15) / 16 * 16 * (kWiD / 8);  // the prefill kernel copies groups of 16 rows
-  for (int c = threadIdx.x; c < n; c += kWiThreads) {
-    const int r = c / (kWiD / 8);
-    uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
-    if (good && r < rows) {
-      const uint32_t wk = kw[r], wv = vw[r];
-      const bool vnan = (wv & 0x7fffu) > 0x7f80u;
-      kx = int4_to_bf16(kc[c], vnan ? 0x7fc0u : wk);
-      if (!vnan) vx = int4_to_bf16(vc[c], wv);
+  for (int c0 = threadIdx.x; c0 < n; c0 += kWiBatch * kWiThreads) {
+    uint32_t wk[kWiBatch], wv[kWiBatch], ck[kWiBatch], cv[kWiBatch];
+    #pragma unroll
+    for (int u = 0; u < kWiBatch; ++u) {  // all loads first
+      const int c = c0 + u * kWiThreads, r = c / (kWiD / 8);
+      wk[u] = wv[u] = ck[u] = cv[u] = 0;  // a row without a key: 0 (0 - 0)
+      if (good && r < rows) {
+        wk[u] = kw[r];
+        wv[u] = vw[r];
+        ck[u] = kc[c];
+        cv[u] = vc[c];
+      }
     }
-    ko[c] = kx;
-    vo[c] = vx;
+    #pragma unroll
+    for (int u = 0; u < kWiBatch; ++u) {
+      const int c = c0 + u * kWiThreads;
+      if (c >= n) break;
+      const bool vnan = (wv[u] & 0x7fffu) > 0x7f80u;
+      ko[c] = int4_to_bf16(ck[u], vnan ? 0x7fc0u : wk[u]);
+      vo[c] = vnan ? make_uint4(0, 0, 0, 0) : int4_to_bf16(cv[u], wv[u]);
+    }
   }
 }
 

@@ -445,6 +445,24 @@ def test_prefill_packed_matches_64_bit_attention(lens, rows, pad):
     _check_prefill(cache, q, rows, out, lse, sm_scale=0.05)
 
 
+def test_prefill_of_single_keys_returns_the_caches_values():
+    # one key a request: its weight is 1, and out is the row of V itself
+    B, Hkv = 40, 4
+    cache = I4.Cache([1] * B, Hkv=Hkv, d=128, P=16, seed=67)
+    rng = np.random.default_rng(68)
+    for b in range(B):
+        pid = cache.table[b, 0]
+        for h in range(Hkv):
+            i = b * Hkv + h                                   # every zero point; scales 2^-40 .. 15 * 2^37
+            s = np.array((8 + i % 8) * 2.0 ** (i % 79 - 42), dtype=np.float32)
+            cache.words[1, pid, h, 0] = I4.word_of(s, i // 8 % 16)
+            cache.pools[1][pid, h, 0] = (np.arange(64) * 37 + 64 * i) % 256 if i % 2 else rng.integers(0, 256, 64)
+    q = I4.bf16(rng.standard_normal((B, Hkv, 128)))
+    out, _ = _prefill(cache, q, [1] * B, uniform=True)
+    want = np.stack([cache.dense(1, b)[:, 0] for b in range(B)])
+    assert np.array_equal(out, want)
+
+
 def test_prefill_nan_rows_bad_pages_and_offsets():
     lens, rows = [200, 150], [100, 150]
     cache = I4.Cache(lens, Hkv=2, d=128, P=16, seed=43)
