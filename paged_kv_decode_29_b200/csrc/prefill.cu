@@ -601,6 +601,7 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
 // The parts of a split prefill into the output: a warp takes one (packed row, q head), lane l head dims
 // 4 l .. 4 l + 3. Rows of one part were written by their CTA; rows behind the last request are left alone.
 constexpr int kPfcThreads = 256;
+constexpr int kPfcAhead = 4;     // parts whose loads are in flight (a divisor of kPfMaxParts)
 constexpr int kPfMaxParts = 32;  // a lane of the combine each
 
 __global__ void __launch_bounds__(kPfcThreads) prefill_combine_kernel(const PrefillParams p) {
@@ -612,12 +613,10 @@ __global__ void __launch_bounds__(kPfcThreads) prefill_combine_kernel(const Pref
   int b, c0, Tb;
   if (p.cu_q) {
     if (row >= p.cu_q[p.B]) return;
-    int a = 0, z = p.B - 1;  // last request with cu_q[b] <= row
-    while (a < z) {
-      const int mid = (a + z + 1) >> 1;
-      if (p.cu_q[mid] <= row) a = mid; else z = mid - 1;
-    }
-    b = a;
+    int upto = 0;  // requests with cu_q[b] <= row: the last of them has the row (a split grid has few requests)
+    for (int i = lane; i - lane < p.B; i += 32) upto += __popc(__ballot_sync(0xffffffffu, i < p.B && p.cu_q[i] <= row));
+    if (upto == 0) return;
+    b = upto - 1;
     c0 = p.cu_q[b];
     Tb = p.cu_q[b + 1] - c0;
     if (c0 < 0 || row < c0 || Tb > p.T || (int64_t)c0 + Tb > p.total_rows) return;  // reported, not written
@@ -633,6 +632,11 @@ __global__ void __launch_bounds__(kPfcThreads) prefill_combine_kernel(const Pref
   const int parts = (nkb + per - 1) / per;
   if (parts <= 1) return;
   const int64_t stride = p.total_rows * p.Hq;
+  const float4* src = reinterpret_cast<const float4*>(p.part_o + item * kPfD) + lane;
+  const int64_t sstep = stride * (kPfD / 4);
+  float4 v[kPfcAhead];  // loads that the weights need not wait for
+  #pragma unroll
+  for (int s = 0; s < kPfcAhead; ++s) v[s] = s < parts ? src[s * sstep] : make_float4(0.f, 0.f, 0.f, 0.f);
   const float my = lane < parts ? p.part_lse[lane * stride + item] : -INFINITY;  // at most kPfMaxParts parts
   float M = my;
   #pragma unroll
@@ -643,10 +647,14 @@ __global__ void __launch_bounds__(kPfcThreads) prefill_combine_kernel(const Pref
   #pragma unroll
   for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < parts; ++s) {
-    const float w = __shfl_sync(0xffffffffu, wgt, s);
-    const float4 v = reinterpret_cast<const float4*>(p.part_o + (s * stride + item) * kPfD)[lane];
-    acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
+  for (int s0 = 0; s0 < parts; s0 += kPfcAhead) {
+    #pragma unroll
+    for (int i = 0; i < kPfcAhead; ++i) {
+      const float w = __shfl_sync(0xffffffffu, wgt, s0 + i);  // 0 past the last part
+      acc.x += w * v[i].x; acc.y += w * v[i].y; acc.z += w * v[i].z; acc.w += w * v[i].w;
+      const int next = s0 + kPfcAhead + i;
+      v[i] = next < parts ? src[next * sstep] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
   }
   const float inv = W == 0.f ? 0.f : 1.f / W;
   reinterpret_cast<uint2*>(p.out_bf16 + item * kPfD)[lane] =
