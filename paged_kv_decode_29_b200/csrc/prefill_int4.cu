@@ -7,9 +7,9 @@
 // a row once; the prefill kernel then reads K and V many times over from L2, and would have to expand
 // them once per query block and head if it did so itself.
 //
-// Measured: 4 x 2048 rows, 32 query heads to 8 KV heads: 172 us, of which the expansion of 22 MB into 67 MB about 8; the rest
+// Measured: 4 x 2048 rows, 32 query heads to 8 KV heads: 170 us, of which the expansion of 9 MB into 34 MB about 8; the rest
 // is the bf16 prefill kernel, bound by the chain of its two products and its softmax. 5 ragged chunks behind histories
-// of up to 7000 keys: 104 us (137 before their keys were split over CTAs).
+// of up to 7000 keys: 90 us (134 with their keys not split over CTAs).
 //
 // A NaN row of V (scale NaN) becomes a NaN row of K and zeros in V: a tensor-core product would carry a
 // NaN of V into rows that do not see the key (0 times NaN), while a NaN score is masked like any other.

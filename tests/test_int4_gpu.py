@@ -445,6 +445,16 @@ def test_prefill_packed_matches_64_bit_attention(lens, rows, pad):
     _check_prefill(cache, q, rows, out, lse, sm_scale=0.05)
 
 
+def test_prefill_of_more_requests_than_lanes_with_split_keys():
+    rng = np.random.default_rng(69)
+    lens = [1000, 300] + [int(x) for x in rng.integers(0, 700, 38)]
+    rows = [min(n, int(x)) for n, x in zip(lens, rng.integers(0, 9, 40))]
+    cache = I4.Cache(lens, Hkv=1, d=128, P=32, seed=70)
+    q = I4.bf16(rng.standard_normal((sum(rows), 2, 128)))
+    out, lse = _prefill(cache, q, rows, uniform=False, max_rows=8, pad=2)
+    _check_prefill(cache, q, rows, out, lse)
+
+
 def test_prefill_of_single_keys_returns_the_caches_values():
     # one key a request: its weight is 1, and out is the row of V itself
     B, Hkv = 40, 4
