@@ -158,6 +158,28 @@ def _stream_handle(stream) -> int | None:
     return h or None
 
 
+def _new(shape, dtype, device, stream, *, result: bool = True) -> torch.Tensor:
+    """An uninitialised tensor for the kernels of a call on ``stream`` (None: the current stream). The allocator hands a
+    freed block back to the stream that it was allocated on, so the memory is taken on the call's own stream: what the
+    call drops on return (``result`` False) is used again only behind its kernels. A result is then used on the current
+    stream, so it is kept until that stream's work on it is done, too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    handle, index = _stream_handle(stream), device.index
+    if index is None:
+        index = torch.cuda.current_device()
+    if handle == _raw_stream(index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # a handle; 0 and 1 (cudaStreamLegacy) are the default stream
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle is not None and handle != 1
+                  else torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -216,7 +238,7 @@ def plan(seq_lens: torch.Tensor, n_kv_heads: int, tile_len: int, max_total_kv_to
     if nbytes == 0:
         raise DecAttnError(ENOTSUP, "dec_attn_plan_bytes")
     if buf is None:
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=seq_lens.device)
+        buf = _new(nbytes, torch.uint8, seq_lens.device, stream)
     h = PlanT()
     rc = lib.dec_attn_plan(_ptr(seq_lens), B, n_kv_heads, tile_len, int(max_total_kv_tokens), n_bins,
                            buf.data_ptr(), buf.numel(), C.byref(h), _stream_handle(stream))
@@ -242,7 +264,7 @@ def plan_sparse(seq_lens: torch.Tensor, tile_mask: torch.Tensor, n_kv_heads: int
     if nbytes == 0:
         raise DecAttnError(ENOTSUP, "dec_attn_plan_sparse_bytes")
     if buf is None:
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=seq_lens.device)
+        buf = _new(nbytes, torch.uint8, seq_lens.device, stream)
     h = PlanT()
     rc = lib.dec_attn_plan_sparse(_ptr(seq_lens), _ptr(tile_mask), int(tile_mask.shape[2]), B, n_kv_heads, tile_len,
                                   int(max_total_kv_tokens), n_bins, buf.data_ptr(), buf.numel(), C.byref(h),
@@ -296,11 +318,11 @@ def run(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_tabl
     shape = make_shape(q, k_pages, page_table, kvt, sm_scale)
     B, T, Hq, d = q.shape
     if out is None:
-        out = torch.empty((B, T, Hq, d), dtype=torch.float32, device=q.device)
+        out = _new((B, T, Hq, d), torch.float32, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
+        lse = _new((B, T, Hq), torch.float32, q.device, stream)
     if workspace is None:
-        workspace = torch.empty(workspace_bytes(shape, pl), dtype=torch.uint8, device=q.device)
+        workspace = _new(workspace_bytes(shape, pl), torch.uint8, q.device, stream, result=False)
     fn = {"run": lib.dec_attn_run, "split": lib.dec_attn_split, "combine": lib.dec_attn_combine}[stage]
     rc = fn(C.byref(shape), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(seq_lens),
             _ptr(kv_scales), C.byref(pl.handle), _ptr(workspace), workspace.numel(), _ptr(out), _ptr(lse),
@@ -340,7 +362,7 @@ def append_rope(q_new: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, p
     lib = load_library()
     shape = make_shape(q_new, k_pages, page_table, kv_dtype_of(k_pages))
     if q_out is None:
-        q_out = torch.empty_like(q_new)
+        q_out = _new(q_new.shape, q_new.dtype, q_new.device, stream)
     rc = lib.dec_attn_append_rope(C.byref(shape), _ptr(q_new), _ptr(k_new), _ptr(v_new), _ptr(page_table),
                                   _ptr(seq_lens), float(rope_base), _ptr(q_out), _ptr(k_pages), _ptr(v_pages),
                                   _ptr(status), _stream_handle(stream))
@@ -361,7 +383,7 @@ def append_rope_fp8(q_new: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tenso
     num_pages, Hkv, P, d2 = k_pages.shape
     shape = ShapeT(B, Hq, Hkv, d, T, P, num_pages, int(page_table.shape[1]), KV_FP8E4M3, 0.0)
     if q_out is None:
-        q_out = torch.empty_like(q_new)
+        q_out = _new(q_new.shape, q_new.dtype, q_new.device, stream)
     rc = lib.dec_attn_append_rope_fp8(C.byref(shape), _ptr(q_new), _ptr(k_new), _ptr(v_new), _ptr(page_table),
                                       _ptr(seq_lens), float(rope_base), _ptr(q_out), _ptr(k_pages), _ptr(v_pages),
                                       _ptr(kv_scales), _ptr(status), _stream_handle(stream))
@@ -381,9 +403,9 @@ def prefill(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_
     shape = make_shape(q, k_pages, page_table, kv_dtype_of(k_pages), sm_scale)
     B, T, Hq, d = q.shape
     if out is None:
-        out = torch.empty((B, T, Hq, d), dtype=torch.float32, device=q.device)
+        out = _new((B, T, Hq, d), torch.float32, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
+        lse = _new((B, T, Hq), torch.float32, q.device, stream)
     rc = lib.dec_attn_prefill(C.byref(shape), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
                               _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(status), _stream_handle(stream))
     if rc != OK:
@@ -404,9 +426,9 @@ def prefill_varlen(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor
     shape = ShapeT(B, Hq, k_pages.shape[1], d, int(max_q_rows), k_pages.shape[2], k_pages.shape[0],
                    page_table.shape[1], kv_dtype_of(k_pages), float(sm_scale))
     if out is None:
-        out = torch.empty((total, Hq, d), dtype=torch.float32, device=q.device)
+        out = _new((total, Hq, d), torch.float32, q.device, stream)
     if lse is None:
-        lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
+        lse = _new((total, Hq), torch.float32, q.device, stream)
     rc = lib.dec_attn_prefill_varlen(C.byref(shape), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
                                      _ptr(seq_lens), _ptr(cu_q_lens), int(total), _ptr(out), _ptr(lse), _ptr(status),
                                      _stream_handle(stream))
@@ -440,11 +462,11 @@ def prefill_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k
     if need < 0:
         raise DecAttnError(need, "dec_attn_prefill_fp8_workspace_bytes")
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(need, 16), torch.uint8, q.device, stream, result=False)
     if out is None:
-        out = torch.empty(out_shape, dtype=torch.float32, device=q.device)
+        out = _new(out_shape, torch.float32, q.device, stream)
     if lse is None:
-        lse = torch.empty(out_shape[:-1], dtype=torch.float32, device=q.device)
+        lse = _new(out_shape[:-1], torch.float32, q.device, stream)
     rc = lib.dec_attn_prefill_fp8(C.byref(shape), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(kv_scales),
                                   _ptr(page_table), _ptr(seq_lens), _ptr(cu_q_lens), int(total), _ptr(workspace),
                                   int(workspace.numel() * workspace.element_size()), _ptr(out), _ptr(lse),
@@ -517,9 +539,9 @@ def _int4_args(rows: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     return ShapeT(B, Hq, Hkv, d, T, P, num_pages, mpps, KV_INT4, 0.0), total, dev
 
 
-def _int4_result(name: str, t: torch.Tensor | None, shape, dtype, like: torch.Tensor) -> torch.Tensor:
+def _int4_result(name: str, t: torch.Tensor | None, shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _new(shape, dtype, like.device, stream)
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
     return t
@@ -546,7 +568,7 @@ def append_rope_int4(q_new: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
     for t in (k_new, v_new, k_values, v_values):
         if t is not None and (t.dtype != _BF16 or t.shape != kv_shape):
             raise ValueError("k_new, v_new and the values are bf16, q_new's rows with Hkv heads")
-    q_out = _int4_result("q_out", q_out, q_new.shape, _BF16, q_new)
+    q_out = _int4_result("q_out", q_out, q_new.shape, _BF16, q_new, stream)
     rc = lib.dec_attn_append_rope_int4(C.byref(shape), q_new.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
                                        page_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_q_lens), total, rope_base,
                                        q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_words.data_ptr(),
@@ -568,10 +590,10 @@ def run_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_w
     if sm_scale:
         shape.sm_scale = sm_scale
     q_shape = q.shape
-    out = _int4_result("out", out, q_shape, _BF16, q)
-    lse = _int4_result("lse", lse, q_shape[:-1], torch.float32, q)
+    out = _int4_result("out", out, q_shape, _BF16, q, stream)
+    lse = _int4_result("lse", lse, q_shape[:-1], torch.float32, q, stream)
     if workspace is None:
-        workspace = torch.empty(workspace_bytes(shape, pl), dtype=torch.uint8, device=q.device)
+        workspace = _new(workspace_bytes(shape, pl), torch.uint8, q.device, stream, result=False)
     rc = lib.dec_attn_run_int4(C.byref(shape), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_words.data_ptr(),
                                page_table.data_ptr(), seq_lens.data_ptr(), C.byref(pl.handle), workspace.data_ptr(),
                                workspace.numel() * workspace.element_size(), out.data_ptr(), lse.data_ptr(),
@@ -595,13 +617,13 @@ def prefill_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     shape.sm_scale = sm_scale
     if cu_q_lens is not None:
         shape.q_tokens = int(max_q_rows)
-    out = _int4_result("out", out, q.shape, _BF16, q)
-    lse = _int4_result("lse", lse, q.shape[:-1], torch.float32, q)
+    out = _int4_result("out", out, q.shape, _BF16, q, stream)
+    lse = _int4_result("lse", lse, q.shape[:-1], torch.float32, q, stream)
     if workspace is None:
         need = lib.dec_attn_prefill_int4_workspace_bytes(C.byref(shape))
         if need < 0:
             raise DecAttnError(need, "dec_attn_prefill_int4_workspace_bytes")
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(need, 16), torch.uint8, q.device, stream, result=False)
     rc = lib.dec_attn_prefill_int4(C.byref(shape), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_words.data_ptr(),
                                    page_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_q_lens), total, workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), out.data_ptr(), lse.data_ptr(), _ptr(status),
