@@ -158,21 +158,28 @@ def _stream_handle(stream) -> int | None:
     return h or None
 
 
+def _other_stream(stream, device):
+    """``stream`` as torch has it, or None where it is the device's current stream (or not given)."""
+    if stream is None:
+        return None
+    handle = _stream_handle(stream)
+    if handle == _raw_stream(torch.cuda.current_device() if device.index is None else device.index):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    # a handle; 0 and 1 (cudaStreamLegacy) are the default stream
+    return (torch.cuda.default_stream(device) if handle is None or handle == 1
+            else torch.cuda.ExternalStream(handle, device=device))
+
+
 def _new(shape, dtype, device, stream, *, result: bool = True) -> torch.Tensor:
     """An uninitialised tensor for the kernels of a call on ``stream`` (None: the current stream). The allocator hands a
     freed block back to the stream that it was allocated on, so the memory is taken on the call's own stream: what the
     call drops on return (``result`` False) is used again only behind its kernels. A result is then used on the current
     stream, so it is kept until that stream's work on it is done, too."""
+    stream = _other_stream(stream, device)
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    handle, index = _stream_handle(stream), device.index
-    if index is None:
-        index = torch.cuda.current_device()
-    if handle == _raw_stream(index):
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):  # a handle; 0 and 1 (cudaStreamLegacy) are the default stream
-        stream = (torch.cuda.ExternalStream(handle, device=device) if handle is not None and handle != 1
-                  else torch.cuda.default_stream(device))
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
     if result:
@@ -667,18 +674,19 @@ def plan_contents(pl: Plan, seq_lens: torch.Tensor, stream=None) -> dict:
     lib = load_library()
     dev = pl.buf.device
     cap = int(pl.handle.max_units)
-    bin_off = torch.empty(pl.n_bins + 1, dtype=torch.int32, device=dev)
-    units = torch.empty((max(cap, 1), 8), dtype=torch.int32, device=dev)
-    n = torch.empty(1, dtype=torch.int32, device=dev)
-    rc = lib.dec_attn_plan_export(C.byref(pl.handle), _ptr(seq_lens), _ptr(bin_off), _ptr(units), cap, _ptr(n),
-                                  _stream_handle(stream))
-    if rc != OK:
-        raise DecAttnError(rc, "dec_attn_plan_export")
-    hdr = pl.buf[:128].cpu().numpy().view(np.int32)
-    n_units = int(n.item())
-    return dict(magic=int(hdr[0]), status=int(hdr[1]), run_status=int(hdr[2]), n_bins=int(hdr[3]),
-                n_units=n_units, bin_off=bin_off.cpu().numpy(),
-                units=units[:max(n_units, 0)].cpu().numpy())
+    with torch.cuda.stream(_other_stream(stream, dev)):  # the copies to the host follow the export; None: as it is
+        bin_off = torch.empty(pl.n_bins + 1, dtype=torch.int32, device=dev)
+        units = torch.empty((max(cap, 1), 8), dtype=torch.int32, device=dev)
+        n = torch.empty(1, dtype=torch.int32, device=dev)
+        rc = lib.dec_attn_plan_export(C.byref(pl.handle), _ptr(seq_lens), _ptr(bin_off), _ptr(units), cap, _ptr(n),
+                                      _stream_handle(stream))
+        if rc != OK:
+            raise DecAttnError(rc, "dec_attn_plan_export")
+        hdr = pl.buf[:128].cpu().numpy().view(np.int32)
+        n_units = int(n.item())
+        return dict(magic=int(hdr[0]), status=int(hdr[1]), run_status=int(hdr[2]), n_bins=int(hdr[3]),
+                    n_units=n_units, bin_off=bin_off.cpu().numpy(),
+                    units=units[:max(n_units, 0)].cpu().numpy())
 
 
 def sm_scale_default(head_dim: int) -> float:

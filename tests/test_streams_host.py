@@ -44,7 +44,7 @@ def world(monkeypatch):
 
     @contextlib.contextmanager
     def use(s):
-        current.append(s)
+        current.append(s or current[-1])
         yield
         current.pop()
     monkeypatch.setattr(torch.cuda, "stream", use)
@@ -118,3 +118,22 @@ def test_buffers_of_a_call_on_the_current_stream(world, name, stream):
     call(stream=stream)
     assert lib.streams == [HERE]
     assert [m[:2] for m in made] == [[HERE, None]] * (results + dropped)
+
+
+@pytest.mark.parametrize("stream,where", [(Stream(THERE), THERE), (THERE, THERE), (HERE, HERE), (None, HERE)])
+def test_a_plans_contents_are_read_behind_their_export(world, monkeypatch, stream, where):
+    lib, made = world
+    pl = da.Plan(buf=torch.zeros(128, dtype=torch.uint8), handle=da.PlanT(n_bins=3, max_units=2))
+    lens, read, cpu, item = torch.ones(2, dtype=torch.int32), [], torch.Tensor.cpu, torch.Tensor.item
+
+    def at(f):
+        def g(t):
+            read.append(torch.cuda.current_stream().cuda_stream)
+            t.zero_() if t.dtype == torch.int32 else None
+            return f(t)
+        return g
+    monkeypatch.setattr(torch.Tensor, "cpu", at(cpu))
+    monkeypatch.setattr(torch.Tensor, "item", at(item))
+    made.clear()
+    assert da.plan_contents(pl, lens, stream=stream)["n_units"] == 0
+    assert lib.streams == [where] and [m[0] for m in made] == [where] * 3 and read == [where] * 4
