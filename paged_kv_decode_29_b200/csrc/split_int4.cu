@@ -11,8 +11,9 @@
 //  * q_r is scaled by a power of two per row, so that its eight significant bits are exact in f16 down to 2^-24
 //    of the row's largest element, and within 2^-35 of that below.
 //  * X is rounded once to f16, relative to a reference of m and of s^V (a power of two near the largest s^V
-//    is divided out, and put back at the end): 2^-11 half a step, an eighth of the rounding that the bf16
-//    output gets anyway. m, l, the zero points' sum, O and the partials are fp32.
+//    is divided out, and put back at the end): off by at most 2^-11 of itself, an eighth of the rounding that the bf16
+//    output gets anyway. Both sums of O take the rounded X, so a key's part of an element is off by that share of
+//    X (c - z), and a channel of zeros stays one. m, l, the zero points' sum, O and the partials are fp32.
 //
 // CTA = W = head_dim / 32 warps, all alike. The KV stream is cut into blocks of 64 keys. Of every block warp w
 // copies keys 64 w / W .. into the rings, computes their scores, and of O holds head dims 32 w .. 32 w + 31 over
@@ -552,7 +553,8 @@ split_int4_kernel(const SplitParams p) {
         const float sc[2] = {vsc[mt][0] * pf, vsc[mt][1] * pf};
         #pragma unroll
         for (int nw = 0; nw < NQ; ++nw) {
-          float pv[4], x[4];
+          float pv[4];
+          uint32_t x[2];
           #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float* v = sv[mt][nw] + 2 * k;
@@ -561,12 +563,12 @@ split_int4_kernel(const SplitParams p) {
             pv[2 * k] = fast_exp2(t0);
             pv[2 * k + 1] = fast_exp2(t1);
             fadd2(lrow[nw][0], lrow[nw][1], lrow[nw][0], lrow[nw][1], pv[2 * k], pv[2 * k + 1]);
-            x[2 * k] = pv[2 * k] * sc[k];
-            x[2 * k + 1] = pv[2 * k + 1] * sc[k];
-            zrow[nw][0] = fmaf(x[2 * k], vz[mt][k], zrow[nw][0]);
-            zrow[nw][1] = fmaf(x[2 * k + 1], vz[mt][k], zrow[nw][1]);
+            x[k] = pack_f16(pv[2 * k] * sc[k], pv[2 * k + 1] * sc[k]);
+            const float2 xf = f16x2_to_float2(x[k]);  // as the product sees them
+            zrow[nw][0] = fmaf(xf.x, vz[mt][k], zrow[nw][0]);
+            zrow[nw][1] = fmaf(xf.y, vz[mt][k], zrow[nw][1]);
           }
-          stsm_x2_t((smb + xs * C::XBUF + nw * 1024 + x_wr) ^ (mt * 32), pack_f16(x[0], x[1]), pack_f16(x[2], x[3]));
+          stsm_x2_t((smb + xs * C::XBUF + nw * 1024 + x_wr) ^ (mt * 32), x[0], x[1]);
         }
       }
     };
