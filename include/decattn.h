@@ -487,8 +487,9 @@ DECATTN_API int dec_attn_append_rope_int4(const dec_attn_shape *shape, const voi
  *   out       bf16 [B][T][Hq][d], 16-byte aligned, rounded once from fp32; lse fp32 [B][T][Hq].
  * Other arguments, shapes, errors and stream rules as dec_attn_run; dense and block-sparse plans (this kernel has no
  * pipeline wait, so it never reports DECATTN_ETIMEOUT). Scores are fp32 sums of exact products of q and the
- * codes; a weight times a V scale is rounded to f16 (2^-11 half a step, where bf16's is 2^-8) for the second
- * product. Slots behind a request's last key, their words among them, may hold anything. A query row that sees a NaN
+ * codes; a weight times a V scale is rounded to f16 for the second product: by at most 2^-11 of itself (bf16's rounding is
+ * 2^-8) or 2^-22 of the largest such number of its query row and tile, whatever the scales of other keys. (V scales further
+ * than 2^12 apart within a tile make the CTA go over its tiles a second time.) Slots behind a request's last key, their words among them, may hold anything. A query row that sees a NaN
  * row of K gets NaN in out and lse, one that sees a NaN row of V in out; no other row does. */
 DECATTN_API int dec_attn_run_int4(const dec_attn_shape *shape, const void *q, const void *k_pages,
                                   const void *v_pages, const void *kv_words, const int32_t *page_table,

@@ -12,7 +12,10 @@
 //    of the row's largest element, and within 2^-35 of that below.
 //  * X is rounded once to f16, relative to a reference of m and of s^V (a power of two near the largest s^V
 //    is divided out, and put back at the end): off by at most 2^-11 of itself, an eighth of the rounding that the bf16
-//    output gets anyway. Both sums of O take the rounded X, so a key's part of an element is off by that share of
+//    output gets anyway, or by 2^-22 of the row's largest X. That holds while a tile's V scales lie within 2^kI4Window of
+//    one another; a tile with others has a reference of X for each row, the largest X that the row has seen, and new
+//    references in every block ("wide": the key whose scale is far out may have no weight, or be hidden from the row).
+//    Both sums of O take the rounded X, so a key's part of an element is off by that share of
 //    X (c - z), and a channel of zeros stays one. m, l, the zero points' sum, O and the partials are fp32.
 //
 // CTA = W = head_dim / 32 warps, all alike. The KV stream is cut into blocks of 64 keys. Of every block warp w
@@ -24,8 +27,8 @@
 // grid: K and V come from L2 for all but one). They decode every code again, but run 16 warps a multiprocessor: 33 to
 // 64 rows held by one CTA (8 warps a multiprocessor, 255 registers) took 46.3 us where this takes 29.7 (56 rows a KV
 // head, 35 requests of 7602 keys together), 17 to 32 rows 31.0 against 27.3.
-//  * One barrier per block, after its scores. It carries a vote whether a score or a V scale passes the
-//    references (m by more than 2^kI4Tau, s^V at all); if so the CTA takes the exact maxima, else they stay.
+//  * One barrier per block, after its scores. It carries a vote whether a score passes its reference by more than
+//    2^kI4Tau, or a V scale lies outside the window; if so the CTA takes the exact maxima, else they stay.
 //    It also makes X of the block before visible, whose product comes next, beside the exponentials of this one.
 //  * The same barrier paces the copies (cp.async): at block g, K (and the row words) of block g + kI4Stages and V
 //    of block g + kI4Stages - 2 go into the places that it has freed, so that every copy has kI4Stages - 1 blocks'
@@ -51,7 +54,11 @@ namespace decattn {
 constexpr int kI4Block = 64;   // keys per block
 constexpr int kI4Stages = 4;   // places of the K ring and of the V ring (a power of two)
 constexpr int kI4Tau = 5;      // P <= 2^kI4Tau
-constexpr int kI4XExp = 9;     // X < 2^(kI4Tau + 1 + kI4XExp) = 2^15; f16's normal range goes 2^23 below P = 1 at the largest s^V
+constexpr int kI4XExp = 9;     // X < 2^(kI4Tau + 1 + kI4XExp) = 2^15
+// V scales that a tile takes with one reference: up to 2^kI4Room above the largest of its first block, and 2^kI4Window in
+// all. The largest X of a row is then 2^(kI4XExp - kI4Window) at least, and f16's subnormal rounding 2^-25.
+constexpr int kI4Room = 4;
+constexpr int kI4Window = 12;
 constexpr int kI4Queue = 64;   // tile descriptors at hand: 32 are fetched at a time
 
 template <int D, int NQ>
@@ -72,7 +79,7 @@ struct I4Cfg {
   static constexpr int OFF_QFRAG = OFF_X + 2 * XBUF;
   static constexpr int OFF_QUEUE = OFF_QFRAG + QFRAG;
   static constexpr int OFF_XCH = OFF_QUEUE + kI4Queue * (int)sizeof(Unit);
-  static constexpr int XCH = 4 * (W * 3 * 8 * NQ + 3 * 8 * NQ + W + 2);  // see the pointers into it
+  static constexpr int XCH = 4 * (W * 5 * 8 * NQ + 3 * 8 * NQ + 2 * W + 3);  // see the pointers into it
   static constexpr int BYTES = (OFF_XCH + XCH + 15) / 16 * 16;
   static constexpr int ALLOC = BYTES + 128;                   // slack to align the base to 128
   // byte offset of (row r, 16-byte chunk c) in a block's K or V codes: the chunks of rows 64 or 32 bytes long are
@@ -114,9 +121,12 @@ __device__ __forceinline__ void stsm_x2_t(uint32_t addr, uint32_t a, uint32_t b)
 // Barrier over the CTA, with a vote.
 __device__ __forceinline__ bool bar_or(bool x) { return __syncthreads_or(x) != 0; }
 
-template <int D, int NQ, int CPS>
-__global__ void __launch_bounds__(I4Cfg<D, NQ>::THREADS, CPS)
-split_int4_kernel(const SplitParams p) {
+// All tiles of the CTA. WIDE: with a reference of X for each row where the V scales of a tile need it; without it such a
+// tile is left wrong, and the return value asks the CTA for a second pass that has it. (One pass for both is slower
+// where no tile needs it, as the hot loop is out of registers: 32 requests of 4096 tokens 42.2 -> 43.2 us, 16 query rows a KV
+// head 105 -> 113. The second pass costs its CTAs the time once more, twice where every tile is wide: 44 -> 91 -> 123.)
+template <int D, int NQ, bool WIDE>
+__device__ __forceinline__ bool i4_pass(const SplitParams& p) {
   using C = I4Cfg<D, NQ>;
   constexpr int W = C::W, MT = C::MT;
   extern __shared__ uint8_t smem_raw[];
@@ -128,16 +138,12 @@ split_int4_kernel(const SplitParams p) {
   float* xmax = reinterpret_cast<float*>(sm + C::OFF_XCH);  // [warp][8 NQ]
   float* xsum = xmax + W * 8 * NQ;                          // [l, zero points][8 NQ][warp]
   float* qrow = xsum + W * 2 * 8 * NQ;                      // [score factor, <1, q>, one over the factor][8 NQ]
-  int* xexp = reinterpret_cast<int*>(qrow + 3 * 8 * NQ);    // [warp]
-  int* n_queued = xexp + W;                                 // [2]: of every other refill
-  // Everything below reads or writes what earlier kernels of the stream may still be working on: the
-  // plan, the pages (a plan serves every layer of a step, so the kernel before this one can be the
-  // append), the combine counters.
-  griddep_wait();
-  griddep_launch_dependents();  // the combine kernel may be scheduled; it waits for this grid itself
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (int64_t)p.B * p.T * p.Hq;
-       i += (int64_t)gridDim.x * blockDim.x)
-    p.row_cnt[i] = 0;
+  int* xexp = reinterpret_cast<int*>(qrow + 3 * 8 * NQ);    // [largest, least][warp]
+  int* n_queued = xexp + 2 * W;                             // [2]: of every other refill
+  int* redo = n_queued + 2;                                 // a second pass is needed
+  float* xtop = reinterpret_cast<float*>(redo + 1);            // [8 NQ][warp]: of a wide tile, the largest X as an exponent
+  int* xrow = redo + 1 + W * 8 * NQ + w * 8 * NQ;       // [warp][8 NQ]: of a wide tile, the references of X
+  if (threadIdx.x == 0) *redo = 0;  // many barriers before its first use
 
   // ======================================================================= tiles
   // The CTA's query rows: r0 .. of every KV head. Its tiles: those of bins blockIdx.x / groups, + gridDim.x / groups,
@@ -298,7 +304,7 @@ split_int4_kernel(const SplitParams p) {
     for (int e = 0; e < 2; ++e) o_rows[nw][e] = row_of(r0 + 8 * nw + 2 * tig + e);
 
   fetch_chunk();
-  if (f_unit < 0) return;  // no tile
+  if (f_unit < 0) return false;  // no tile
   load_q(queue[0]);        // beside the first copies
   #pragma unroll
   for (int i = 0; i < kI4Stages; ++i) copy_step(i, i >= 2);
@@ -361,8 +367,11 @@ split_int4_kernel(const SplitParams p) {
     float o[NQ][2][4];
     float nmu[NQ][2], thr[NQ][2];    // minus the reference m (0 for none yet), the score that moves it
     float lrow[NQ][2], zrow[NQ][2];  // this lane's keys' shares of l and of the zero points' sum
-    int eref = 16;  // biased exponent that X is relative to (of the largest s^V so far; at least 2^-111)
-    float sref = __int_as_float(17 << 23);  // the first scale above that
+    // X's reference is 2^(eref - 127), in a wide tile xrow's for each row; the scales that it serves have bit
+    // patterns from slow up to slow + swin (a negative or NaN scale never has one)
+    int eref = 16;
+    uint32_t slow = 0, swin = 0;
+    bool wide = false;
     #pragma unroll
     for (int nw = 0; nw < NQ; ++nw)
       #pragma unroll
@@ -469,8 +478,8 @@ split_int4_kernel(const SplitParams p) {
           }
         }
         #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (j0 + 8 * k >= d.tok_end || vsc[mt][k] != vsc[mt][k]) vsc[mt][k] = 0.f;
+        for (int k = 0; k < 2; ++k)  // P is 0: any scale of the window
+          if (j0 + 8 * k >= d.tok_end || vsc[mt][k] != vsc[mt][k]) vsc[mt][k] = __uint_as_float(slow);
       }
       asm volatile("" ::: "memory");  // a branch, not predicated instructions in every block
     };
@@ -482,7 +491,7 @@ split_int4_kernel(const SplitParams p) {
       if (kbase + kI4Block > safe_end) mask_block(kbase);
       #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        over |= vsc[mt][0] >= sref || vsc[mt][1] >= sref;
+        over |= __float_as_uint(vsc[mt][0]) - slow >= swin || __float_as_uint(vsc[mt][1]) - slow >= swin;
         #pragma unroll
         for (int nw = 0; nw < NQ; ++nw)
           over |= fmaxf(sv[mt][nw][0], sv[mt][nw][2]) > thr[nw][0] || fmaxf(sv[mt][nw][1], sv[mt][nw][3]) > thr[nw][1];
@@ -490,8 +499,8 @@ split_int4_kernel(const SplitParams p) {
       cp_async_wait<kI4Stages - 2>();
       return bar_or(over);
     };
-    // New references: the exact maxima of the rows and of the V scales' exponents.
-    auto new_references = [&] {
+    // New references: the exact maxima of the rows; of X from the first block's scales, or row by row.
+    auto new_references = [&](bool first) {
       #pragma unroll
       for (int nw = 0; nw < NQ; ++nw)
         #pragma unroll
@@ -504,39 +513,96 @@ split_int4_kernel(const SplitParams p) {
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           if (gid == 0) xmax[w * 8 * NQ + 8 * nw + 2 * tig + e] = mx;
         }
-      int ev = 0;
+      // exponents of the V scales: NaN rows do not count, nor does 0 (a key that no row sees); a negative scale, which no
+      // append writes, is below them all
+      int e_hi = 0, e_lo = 255;
       #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
         #pragma unroll
-        for (int k = 0; k < 2; ++k) {  // a NaN row of V does not count
-          const int e = __float_as_int(vsc[mt][k]) >> 23 & 0xff;
-          ev = max(ev, e == 0xff ? 0 : e);
+        for (int k = 0; k < 2; ++k) {
+          const int e = __float_as_int(vsc[mt][k]) >> 23;
+          if ((e & 0xff) != 0xff && (e & 0xff) != 0) {
+            e_hi = max(e_hi, e);
+            e_lo = min(e_lo, e);
+          }
         }
-      ev = __reduce_max_sync(0xffffffffu, ev);
-      if (lane == 0) xexp[w] = ev;
+      e_hi = __reduce_max_sync(0xffffffffu, e_hi);
+      e_lo = __reduce_min_sync(0xffffffffu, e_lo);
+      if (lane == 0) {
+        xexp[w] = e_hi;
+        xexp[W + w] = e_lo;
+      }
       __syncthreads();
-      int enew = eref;
       #pragma unroll
-      for (int i = 0; i < W; ++i) enew = max(enew, xexp[i]);
-      const int de = eref - enew;  // <= 0
-      const float es = de < -126 ? 0.f : __int_as_float((127 + de) << 23);
-      eref = enew;
-      sref = eref == 254 ? INFINITY : __int_as_float((eref + 1) << 23);
+      for (int i = 0; i < W; ++i) {
+        e_hi = max(e_hi, xexp[i]);
+        e_lo = min(e_lo, xexp[W + i]);
+      }
+      [[maybe_unused]] const bool was_wide = wide;
+      if (first) {
+        eref = min(max(e_hi + kI4Room, 16), 254);
+        slow = eref == 16 ? 0u : (uint32_t)(eref - kI4Window) << 23;  // below 2^-111 there is nothing to lose
+        swin = ((uint32_t)(eref + 1) << 23) - slow;
+      }
+      if (!wide && (e_lo < (int)(slow >> 23) || e_hi > eref)) {
+        if constexpr (WIDE) {
+          wide = true;
+          swin = 0;  // every vote asks for new references
+        } else {
+          *redo = 1;
+        }
+      }
+      [[maybe_unused]] float mx2[NQ][2];  // largest s^V 2^S of the rows, as an exponent
+      if (WIDE && wide) {
+        #pragma unroll
+        for (int nw = 0; nw < NQ; ++nw)
+          #pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = -INFINITY;
+            #pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              #pragma unroll
+              for (int k = 0; k < 2; ++k)
+                mx = fmaxf(mx, fmaf(sv[mt][nw][2 * k + e], fcol[nw][e], (float)(__float_as_int(vsc[mt][k]) >> 23 & 0xff)));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            if (gid == 0) xtop[(8 * nw + 2 * tig + e) * W + w] = mx;
+          }
+        __syncthreads();
+        #pragma unroll
+        for (int nw = 0; nw < NQ; ++nw)
+          #pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mx2[nw][e] = -INFINITY;
+            #pragma unroll
+            for (int i = 0; i < W; ++i) mx2[nw][e] = fmaxf(mx2[nw][e], xtop[(8 * nw + 2 * tig + e) * W + i]);
+          }
+      }
       #pragma unroll
       for (int nw = 0; nw < NQ; ++nw)
         #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = xmax[8 * nw + 2 * tig + e];
+          const int col = 8 * nw + 2 * tig + e;
+          float mx = xmax[col];
           #pragma unroll
-          for (int i = 1; i < W; ++i) mx = fmaxf(mx, xmax[i * 8 * NQ + 8 * nw + 2 * tig + e]);
+          for (int i = 1; i < W; ++i) mx = fmaxf(mx, xmax[i * 8 * NQ + col]);
           const float mold = thr[nw][e] == -INFINITY ? -INFINITY : -nmu[nw][e];
           const float mnew = fmaxf(mold, mx * fcol[nw][e]);  // the factor is positive
           const float mu = mnew == -INFINITY ? 0.f : mnew;
           const float alpha = fast_exp2(mold - mu);
+          float a = alpha;
+          if (WIDE && wide) {
+            const int eold = was_wide ? xrow[col] : eref;
+            const float top = fmaxf(mold + (float)eold, mx2[nw][e]) - mu;  // exponent of the largest X so far
+            const int enew = top > 16.f ? (int)ceilf(fminf(top, 254.f)) : 16;
+            a = fast_exp2(mold - mu + (float)(eold - enew));
+            __syncwarp();  // all lanes have the old one
+            if (gid == 0) xrow[col] = enew;
+          }
           nmu[nw][e] = -mu;
-          thr[nw][e] = mnew == -INFINITY ? -INFINITY : (mnew + (float)kI4Tau) * qrow[16 * NQ + 8 * nw + 2 * tig + e];
+          thr[nw][e] = mnew == -INFINITY ? -INFINITY : (mnew + (float)kI4Tau) * qrow[16 * NQ + col];
           lrow[nw][e] *= alpha;
-          const float a = alpha * es;
           zrow[nw][e] *= a;
           #pragma unroll
           for (int jj = 0; jj < 2; ++jj) {
@@ -544,6 +610,7 @@ split_int4_kernel(const SplitParams p) {
             o[nw][jj][e + 2] *= a;
           }
         }
+      if constexpr (WIDE) __syncwarp();
     };
     // X of this warp's keys, to buffer xs
     auto weights = [&](int xs) {
@@ -573,6 +640,31 @@ split_int4_kernel(const SplitParams p) {
       }
     };
 
+    // ... in a wide tile: X = 2^(S - m + exponents) times the scale's significand, so that neither factor alone leaves
+    // fp32's range
+    [[maybe_unused]] auto weights_wide = [&](int xs) {
+      #pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        #pragma unroll
+        for (int nw = 0; nw < NQ; ++nw) {
+          float x[4];
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t sb = __float_as_uint(vsc[mt][i >> 1]);
+            const int ev = max((int)(sb >> 23 & 0xff), 1);
+            const float sig = (sb & 0x7f800000u) == 0 ? vsc[mt][i >> 1] * 0x1p126f : __uint_as_float((sb & 0x807fffffu) | 0x3f800000u);
+            const float t = fmaf(sv[mt][nw][i], fcol[nw][i & 1], nmu[nw][i & 1]);
+            lrow[nw][i & 1] += fast_exp2(t);
+            x[i] = fast_exp2(t + (float)(ev - xrow[8 * nw + 2 * tig + (i & 1)] + kI4XExp)) * sig;
+          }
+          const uint32_t x0 = pack_f16(x[0], x[1]), x1 = pack_f16(x[2], x[3]);
+          const float2 f0 = f16x2_to_float2(x0), f1 = f16x2_to_float2(x1);
+          zrow[nw][0] += f0.x * vz[mt][0] + f1.x * vz[mt][1];
+          zrow[nw][1] += f0.y * vz[mt][0] + f1.y * vz[mt][1];
+          stsm_x2_t((smb + xs * C::XBUF + nw * 1024 + x_wr) ^ (mt * 32), x0, x1);
+        }
+    };
+
     const int nblk = uniform(n_blocks(d));
     int kbase = d.tok_begin;
     scores(g % kI4Stages);
@@ -584,19 +676,21 @@ split_int4_kernel(const SplitParams p) {
       copy_step(g % kI4Stages, true);
       if (over || blk == 0) {
         if (blk > 0) product((g - 1) % kI4Stages, (blk - 1) & 1);
-        new_references();
+        new_references(blk == 0);
       } else {
         product((g - 1) % kI4Stages, (blk - 1) & 1);
       }
-      weights(blk & 1);
+      if (WIDE && wide) weights_wide(blk & 1);
+      else weights(blk & 1);
       scores((g + 1) % kI4Stages);
       kbase += kI4Block;
       over = vote(kbase);
     }
     copy_step(g % kI4Stages, true);
     if (nblk > 1) product((g - 1) % kI4Stages, nblk & 1);
-    if (over || nblk == 1) new_references();
-    weights((nblk - 1) & 1);
+    if (over || nblk == 1) new_references(nblk == 1);
+    if (WIDE && wide) weights_wide((nblk - 1) & 1);
+    else weights((nblk - 1) & 1);
     ++g;
     // ---- sums over the keys: of a warp's lanes, then of the warps
     #pragma unroll
@@ -620,7 +714,6 @@ split_int4_kernel(const SplitParams p) {
 
     if (unit + 1 <= f_unit) load_q(queue[(unit + 1) % kI4Queue]);  // beside the epilogue
     // ---- epilogue: normalise, store. O is in units of 2^(eref - 127 - kI4XExp): codes and X exactly so
-    const float unref = __int_as_float((eref - kI4XExp) << 23);  // eref >= 16
     #pragma unroll
     for (int nw = 0; nw < NQ; ++nw)
       #pragma unroll
@@ -633,6 +726,7 @@ split_int4_kernel(const SplitParams p) {
           z += xs[8 * NQ * W + i];
         }
         if (o_rows[nw][e] < 0) continue;
+        const float unref = __int_as_float(((WIDE && wide ? xrow[8 * nw + 2 * tig + e] : eref) - kI4XExp) << 23);  // 16 at least
         const float inv = l == 0.f ? 0.f : unref / l;
         const float lse_v = l == 0.f ? -INFINITY : (__log2f(l) - nmu[nw][e]) * LN2;
         const float v[4] = {fmaf(o[nw][0][e], 16777216.f, -z) * inv, fmaf(o[nw][0][e + 2], 1048576.f, -z) * inv,
@@ -649,6 +743,28 @@ split_int4_kernel(const SplitParams p) {
       }
   }
   cp_async_wait<0>();  // copies past the last block
+  __syncthreads();
+  return *redo != 0;
+}
+
+template <int D, int NQ>
+__device__ __noinline__ void i4_wide_pass(const SplitParams& p) {
+  __syncthreads();  // the first pass is done with the shared memory
+  i4_pass<D, NQ, true>(p);
+}
+
+template <int D, int NQ, int CPS>
+__global__ void __launch_bounds__(I4Cfg<D, NQ>::THREADS, CPS)
+split_int4_kernel(const __grid_constant__ SplitParams p) {
+  // Everything below reads or writes what earlier kernels of the stream may still be working on: the
+  // plan, the pages (a plan serves every layer of a step, so the kernel before this one can be the
+  // append), the combine counters.
+  griddep_wait();
+  griddep_launch_dependents();  // the combine kernel may be scheduled; it waits for this grid itself
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (int64_t)p.B * p.T * p.Hq;
+       i += (int64_t)gridDim.x * blockDim.x)
+    p.row_cnt[i] = 0;
+  if (i4_pass<D, NQ, false>(p)) i4_wide_pass<D, NQ>(p);
 }
 
 // ------------------------------------------------------------------ host side

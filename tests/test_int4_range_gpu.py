@@ -17,6 +17,79 @@ def _set_row(cache, which, b, h, pos, word, codes=None):
         cache.pools[which][pid, h, slot] = codes
 
 
+def _add_exponent(cache, which, b, h, pos, k):
+    """That row's scale times 2^k."""
+    pid, slot = cache.table[b, pos // cache.P], pos % cache.P
+    cache.words[which, pid, h, slot] = int(cache.words[which, pid, h, slot]) + (k << 7)
+
+
+# ---------------------------------------------------------------------------- V scales that lie far apart
+@pytest.mark.parametrize("k", [4, 11, 20, 24, 28, 34, 40, 60, 100])
+@pytest.mark.parametrize("d,pos", [(128, 5), (128, 150), (64, 150), (128, 199)])
+def test_a_large_v_row_of_no_weight_takes_nothing_from_the_others(d, pos, k):
+    cache = I4.Cache([200], Hkv=1, d=d, P=16, seed=101)
+    q = I4.bf16(np.abs(np.random.default_rng(102).standard_normal((1, 1, 4, d))) + 0.1)
+    _set_row(cache, 0, 0, 0, pos, 0x40FF, 0)                 # K: -15 times 7.5 in every channel: a weight below 2^-200
+    _add_exponent(cache, 1, 0, 0, pos, k)
+    for tile in (64, 256):
+        out, lse = _decode(cache, q, 1, tile=tile)
+        _check_decode(cache, q, 1, out, lse, what=f"tile {tile}")
+
+
+@pytest.mark.parametrize("k", [11, 24, 28, 34, 60, 100, -40, -100])
+@pytest.mark.parametrize("hq,d", [(4, 128), (4, 64), (2, 128)])
+def test_rows_do_not_depend_on_the_v_rows_of_later_tokens(hq, d, k):
+    T, L = 4, 130
+    cache = I4.Cache([L, 3], Hkv=1, d=d, P=16, seed=103)
+    q = I4.bf16(np.random.default_rng(104).standard_normal((2, T, hq, d)))
+    for b, n in enumerate(cache.lens):
+        _add_exponent(cache, 1, b, 0, n - 1, k)              # the last token: seen by the last row alone
+    for tile in (64, 256):
+        out, lse = _decode(cache, q, T, tile=tile)
+        _check_decode(cache, q, T, out, lse, what=f"tile {tile}")
+
+
+@pytest.mark.parametrize("span", [5, 12, 25, 60, 110])
+@pytest.mark.parametrize("hq,T,d", [(4, 1, 128), (4, 4, 64), (8, 5, 128)])
+def test_v_scales_of_any_spread(hq, T, d, span):
+    """Every row's scale times a power of two of its own; equal weights, and queries that pick out single keys, each
+    with the scale of its own key."""
+    lens = [300, 65, 1000]
+    cache = I4.Cache(lens, Hkv=2, d=d, P=16, seed=105 + span)
+    rng = np.random.default_rng(106)
+    w = cache.words[1].astype(np.int64)
+    w += rng.integers(-span, span + 1, w.shape) << 7
+    for b, n in enumerate(lens):
+        for i, pid in enumerate(cache.table[b, :-(-n // 16)]):
+            used = min(16, n - 16 * i)
+            cache.words[1, pid, :, :used] = w[pid, :, :used]
+    q = rng.standard_normal((3, T, hq, d))
+    for b, n in enumerate(lens):
+        k = cache.dense(0, b)
+        for t in range(T):
+            for h in range(0, hq, 2):
+                q[b, t, h] = 100 * np.sign(k[h // (hq // 2), rng.integers(0, n - T + 1)])
+    q = I4.bf16(q)
+    for tile in (64, 1024):
+        out, lse = _decode(cache, q, T, tile=tile)
+        _check_decode(cache, q, T, out, lse, what=f"tile {tile}")
+
+
+def test_zero_v_rows_among_others():
+    """An all-zero row is stored with the least scale there is."""
+    cache = I4.Cache([400], Hkv=1, d=128, P=16, seed=107)
+    for pos in (0, 1, 2, 63, 64, 200, 399):
+        _set_row(cache, 1, 0, 0, pos, 0x0080, 0)
+    q = I4.bf16(np.random.default_rng(108).standard_normal((1, 1, 8, 128)))
+    for tile in (64, 512):
+        out, lse = _decode(cache, q, 1, tile=tile)
+        _check_decode(cache, q, 1, out, lse, what=f"tile {tile}")
+    cache.words[1] = 0x0080                                  # and nothing else
+    cache.pools[1][:] = 0
+    out, _ = _decode(cache, q, 1, tile=512)
+    assert np.all(out == 0)
+
+
 # ---------------------------------------------------------------------------- weights and zero points
 @pytest.mark.parametrize("d", [64, 128])
 def test_a_channel_of_zeros_comes_out_near_zero(d):
