@@ -97,7 +97,8 @@ typedef enum {
  *          bits of byte i, element 2 i + 1 in the high four;
  *   words  kv_words: uint16 [2][num_pages][Hkv][P] (K, then V), one per row: the word with its four low bits
  *          cleared is the row's scale s as a bf16 bit pattern, its four low bits are the zero point z.
- * Element i of a row is s (c_i - z). The scale has at most four significant bits, so every element is a
+ * Element i of a row is s (c_i - z); a row whose scale is NaN is a NaN row (an infinite scale, which no append
+ * writes, makes a row of V one, too). The scale has at most four significant bits, so every element is a
  * bf16 number exactly. 4 bits an element and 16 a row: 66 bytes where bf16 takes 256 (head_dim 128).
  * dec_attn_append_rope_int4 writes such a cache, dec_attn_run_int4 and dec_attn_prefill_int4 read it; their
  * out is bf16 (the cache's own rounding is about 2^-4 of a row's range). The planners, their plan buffers
@@ -490,7 +491,7 @@ DECATTN_API int dec_attn_append_rope_int4(const dec_attn_shape *shape, const voi
  * codes; a weight times a V scale is rounded to f16 for the second product: by at most 2^-11 of itself (bf16's rounding is
  * 2^-8) or 2^-22 of the largest such number of its query row and tile, whatever the scales of other keys. (V scales further
  * than 2^12 apart within a tile make the CTA go over its tiles a second time.) Slots behind a request's last key, their words among them, may hold anything. A query row that sees a NaN
- * row of K gets NaN in out and lse, one that sees a NaN row of V in out; no other row does. */
+ * row of K or V gets NaN in out and lse; no other row does. */
 DECATTN_API int dec_attn_run_int4(const dec_attn_shape *shape, const void *q, const void *k_pages,
                                   const void *v_pages, const void *kv_words, const int32_t *page_table,
                                   const int32_t *seq_lens, const dec_attn_plan_t *plan, void *workspace,

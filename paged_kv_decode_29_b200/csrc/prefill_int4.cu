@@ -11,7 +11,7 @@
 // is the bf16 prefill kernel, bound by the chain of its two products and its softmax. 5 ragged chunks behind histories
 // of up to 7000 keys: 90 us (134 with their keys not split over CTAs).
 //
-// A NaN row of V (scale NaN) becomes a NaN row of K and zeros in V: a tensor-core product would carry a
+// A NaN row of V (scale not finite) becomes a NaN row of K and zeros in V: a tensor-core product would carry a
 // NaN of V into rows that do not see the key (0 times NaN), while a NaN score is masked like any other.
 #include "common.cuh"
 #include "int4.cuh"
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kWiThreads) widen_int4_kernel(const WidenInt4P
     for (int u = 0; u < kWiBatch; ++u) {
       const int c = c0 + u * kWiThreads;
       if (c >= n) break;
-      const bool vnan = (wv[u] & 0x7fffu) > 0x7f80u;
+      const bool vnan = (wv[u] & 0x7f80u) == 0x7f80u;
       ko[c] = int4_to_bf16(ck[u], vnan ? 0x7fc0u : wk[u]);
       vo[c] = vnan ? make_uint4(0, 0, 0, 0) : int4_to_bf16(cv[u], wv[u]);
     }

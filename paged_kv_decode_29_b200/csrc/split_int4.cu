@@ -460,26 +460,29 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
             sv[mt][nw][i] = fmaf(kz[i >> 1], qsum[nw][i & 1], sv[mt][nw][i]) * ksc[i >> 1];
       }
     };
+    // A NaN row of V moves into the scores of the query rows that see it: out and lse are NaN as for one of K, and 0
+    // times its NaN reaches no other row. Its scale is in no window, so a block that all rows see comes to
+    // new_references() for it.
+    auto not_finite = [](float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; };
     // A block that not every row sees to its end: scores of invisible keys become -inf, whatever their words
-    // and codes hold. A NaN row of V moves into the scores of the rows that see it, so that 0 times its NaN
-    // reaches no other.
+    // and codes hold.
     auto mask_block = [&](int kbase) {
       #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const int j0 = kbase + 16 * (w * MT + mt) + gid;
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bool bad = vsc[mt][i >> 1] != vsc[mt][i >> 1];
+          const bool bad = not_finite(vsc[mt][i >> 1]);
           #pragma unroll
           for (int nw = 0; nw < NQ; ++nw) {
             const int r = r0 + 8 * nw + 2 * tig + (i & 1), j = j0 + (i >> 1) * 8;
             if (j >= d.tok_end || (r < p.GT && j > d.seq_len - p.T + r / p.G)) sv[mt][nw][i] = -INFINITY;
-            else if (bad) sv[mt][nw][i] = vsc[mt][i >> 1];
+            else if (bad) sv[mt][nw][i] = __int_as_float(0x7fc00000);
           }
         }
         #pragma unroll
         for (int k = 0; k < 2; ++k)  // P is 0: any scale of the window
-          if (j0 + 8 * k >= d.tok_end || vsc[mt][k] != vsc[mt][k]) vsc[mt][k] = __uint_as_float(slow);
+          if (j0 + 8 * k >= d.tok_end || not_finite(vsc[mt][k])) vsc[mt][k] = __uint_as_float(slow);
       }
       asm volatile("" ::: "memory");  // a branch, not predicated instructions in every block
     };
@@ -502,6 +505,15 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
     // New references: the exact maxima of the rows; of X from the first block's scales, or row by row.
     auto new_references = [&](bool first) {
       #pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        #pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (not_finite(vsc[mt][k])) {
+            #pragma unroll
+            for (int nw = 0; nw < NQ; ++nw) sv[mt][nw][2 * k] = sv[mt][nw][2 * k + 1] = __int_as_float(0x7fc00000);
+            vsc[mt][k] = __uint_as_float(slow);
+          }
+      #pragma unroll
       for (int nw = 0; nw < NQ; ++nw)
         #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -513,15 +525,15 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           if (gid == 0) xmax[w * 8 * NQ + 8 * nw + 2 * tig + e] = mx;
         }
-      // exponents of the V scales: NaN rows do not count, nor does 0 (a key that no row sees); a negative scale, which no
-      // append writes, is below them all
+      // exponents of the V scales: 0 (a key that no row sees) does not count; a negative scale, which no append
+      // writes, is below them all
       int e_hi = 0, e_lo = 255;
       #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
         #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int e = __float_as_int(vsc[mt][k]) >> 23;
-          if ((e & 0xff) != 0xff && (e & 0xff) != 0) {
+          if ((e & 0xff) != 0) {
             e_hi = max(e_hi, e);
             e_lo = min(e_lo, e);
           }

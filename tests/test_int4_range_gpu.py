@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from tests import _int4 as I4
-from tests.test_int4_gpu import _check_decode, _decode
+from tests.test_int4_gpu import _check_decode, _decode, _prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +111,39 @@ def test_a_channel_of_zeros_comes_out_near_zero(d):
     out, lse = _decode(cache, q, 1, tile=256, sm_scale=0.3)
     _check_decode(cache, q, 1, out, lse, sm_scale=0.3)
     assert np.abs(out[..., ::4]).max() <= 15 * (17 * 16 * 2.0 ** -23 + 2.0 ** -19)
+
+
+# ---------------------------------------------------------------------------- NaN rows
+@pytest.mark.parametrize("tile", [64, 512])
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("word", [0x7FC0, 0xFFC0])
+def test_a_nan_row_reaches_out_and_lse_wherever_it_lies(word, which, tile):
+    T, L = 2, 300
+    cache = I4.Cache([L, 40], Hkv=2, d=128, P=16, seed=110)
+    q = I4.bf16(np.random.default_rng(111).standard_normal((2, T, 4, 128)))
+    ref, ref_l = _decode(cache, q, T, tile=tile)
+    for pos in (0, 70, 192, 255, 297, 299):                  # first and later blocks, the masked last one
+        pid, slot = cache.table[0, pos // 16], pos % 16
+        saved = cache.words[which, pid, 1, slot]
+        cache.words[which, pid, 1, slot] = word
+        out, lse = _decode(cache, q, T, tile=tile)
+        cache.words[which, pid, 1, slot] = saved
+        sees = np.zeros(out.shape[:3], dtype=bool)
+        sees[0, :, 2:] = (L - T + np.arange(T) >= pos)[:, None]
+        assert np.isnan(out[sees]).all() and np.isnan(lse[sees]).all(), pos
+        assert np.array_equal(out[~sees], ref[~sees]) and np.array_equal(lse[~sees], ref_l[~sees]), pos
+
+
+def test_an_infinite_v_scale_is_a_nan_row():
+    cache = I4.Cache([200], Hkv=1, d=128, P=16, seed=112)
+    q = I4.bf16(np.random.default_rng(113).standard_normal((1, 3, 4, 128)))
+    ref, ref_l = _decode(cache, q, 3, tile=256)
+    pref, pref_l = _prefill(cache, q[0], [3], uniform=True)
+    for word in (0x7F80, 0x7F83, 0xFF80):
+        _set_row(cache, 1, 0, 0, 198, word)
+        out, lse = _decode(cache, q, 3, tile=256)
+        assert np.isnan(out[0, 1:]).all() and np.isnan(lse[0, 1:]).all()
+        assert np.array_equal(out[0, 0], ref[0, 0]) and np.array_equal(lse[0, 0], ref_l[0, 0])
+        out, lse = _prefill(cache, q[0], [3], uniform=True)
+        assert np.isnan(out[1:]).all() and np.isnan(lse[1:]).all()
+        assert np.array_equal(out[0], pref[0]) and np.array_equal(lse[0], pref_l[0])
