@@ -349,10 +349,10 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
             make_uint4(pack_f16(v[0], v[4]), pack_f16(v[1], v[5]), pack_f16(v[2], v[6]), pack_f16(v[3], v[7]));
         #pragma unroll
         for (int k = 1; k < LPQ; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-        if (sg == 0) {  // a row that is not finite has NaN scores
-          const float f = amax >= 0x7f80u ? __int_as_float(0x7fc00000) : __int_as_float((127 + 24 - E) << 23) * p.qk_scale_log2;
+        if (sg == 0) {  // a row that is not finite has NaN scores where it sees a key; the mask comes after them
+          const float f = amax >= 0x7f80u ? 1.f : __int_as_float((127 + 24 - E) << 23) * p.qk_scale_log2;
           qrow[row] = f;
-          qrow[8 * NQ + row] = sum * 0x1p-24f;
+          qrow[8 * NQ + row] = amax >= 0x7f80u ? __int_as_float(0x7fc00000) : sum * 0x1p-24f;
           qrow[16 * NQ + row] = 1.f / f;
         }
       }

@@ -147,3 +147,33 @@ def test_an_infinite_v_scale_is_a_nan_row():
         out, lse = _prefill(cache, q[0], [3], uniform=True)
         assert np.isnan(out[1:]).all() and np.isnan(lse[1:]).all()
         assert np.array_equal(out[0], pref[0]) and np.array_equal(lse[0], pref_l[0])
+
+
+# ---------------------------------------------------------------------------- queries
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_a_query_row_that_is_not_finite_stays_alone(bad):
+    """... and has out = 0 and lse = -inf like any other where it sees no key. Where it sees some, decode gives NaN; so does
+    prefill, but for a row all of whose scores are -inf (an infinite element times keys of one sign), which has no weight
+    anywhere and comes out like a row without a key, as over the other caches."""
+    T, lens = 4, [2, 130, 1]
+    cache = I4.Cache(lens, Hkv=2, d=128, P=16, seed=114)
+    q = I4.bf16(np.random.default_rng(115).standard_normal((3, T, 4, 128)))
+    x = q.copy()
+    x[0, 1, 0, 5] = x[0, 0, 3] = x[0, 2, 2, 127] = x[1, 0, 1, 64] = x[1, 3] = x[2, :3, 0, 0] = bad
+    hit = ~np.isfinite(x).all(-1)
+    empty = np.array([[n - T + t < 0 for t in range(T)] for n in lens])[:, :, None] & np.ones((1, 1, 4), dtype=bool)
+    pre = [[y.reshape(q.shape[:y.ndim + 1]) for y in _prefill(cache, z.reshape(12, 4, 128), [T] * 3, uniform=True)] for z in (q, x)]
+    for ref, got in ((_decode(cache, q, T, tile=64), _decode(cache, x, T, tile=64)), pre):
+        assert np.all(got[0][empty] == 0) and np.all(np.isneginf(got[1][empty]))
+        assert np.array_equal(got[0][~hit], ref[0][~hit]) and np.array_equal(got[1][~hit], ref[1][~hit])
+        nan = hit & ~empty
+        if got is pre[1]:
+            with np.errstate(invalid="ignore"):
+                for b, n in enumerate(lens):
+                    for t in range(T):
+                        for h in range(4):
+                            s = cache.dense(0, b)[h // 2, :max(n - T + t + 1, 0)] * x[b, t, h]
+                            if nan[b, t, h] and np.all(np.isneginf(s.sum(-1))):
+                                nan[b, t, h] = False
+                                assert np.all(got[0][b, t, h] == 0) and np.isneginf(got[1][b, t, h])
+        assert np.isnan(got[0][nan]).all() and np.isnan(got[1][nan]).all()
