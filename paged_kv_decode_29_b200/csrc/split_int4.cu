@@ -8,7 +8,7 @@
 // The tensor cores see codes, untouched but for a mask: a code in bits 0 .. 3 or 4 .. 7 of a half-word is the f16
 // number c 2^-24 or c 2^-20 (a subnormal). Scales and zero points act on one score or one weight instead of on
 // head_dim elements.
-//  * q_r is scaled by a power of two per row, so that its eight significant bits are exact in f16 down to 2^-24
+//  * q_r, of any magnitude, is scaled by a power of two per row, so that its eight significant bits are exact in f16 down to 2^-24
 //    of the row's largest element, and within 2^-35 of that below.
 //  * X is rounded once to f16, relative to a reference of m and of s^V (a power of two near the largest s^V
 //    is divided out, and put back at the end): off by at most 2^-11 of itself, an eighth of the rounding that the bf16
@@ -59,6 +59,7 @@ constexpr int kI4XExp = 9;     // X < 2^(kI4Tau + 1 + kI4XExp) = 2^15
 // all. The largest X of a row is then 2^(kI4XExp - kI4Window) at least, and f16's subnormal rounding 2^-25.
 constexpr int kI4Room = 4;
 constexpr int kI4Window = 12;
+constexpr float kI4Far = 0x1p20f;  // |m| from which S - m is taken the other way: here m is off by up to 2^-4, and P by 2^(2^-4)
 constexpr int kI4Queue = 64;   // tile descriptors at hand: 32 are fetched at a time
 
 template <int D, int NQ>
@@ -79,7 +80,7 @@ struct I4Cfg {
   static constexpr int OFF_QFRAG = OFF_X + 2 * XBUF;
   static constexpr int OFF_QUEUE = OFF_QFRAG + QFRAG;
   static constexpr int OFF_XCH = OFF_QUEUE + kI4Queue * (int)sizeof(Unit);
-  static constexpr int XCH = 4 * (W * 5 * 8 * NQ + 3 * 8 * NQ + 2 * W + 3);  // see the pointers into it
+  static constexpr int XCH = 4 * (W * 5 * 8 * NQ + 4 * 8 * NQ + 2 * W + 3);  // see the pointers into it
   static constexpr int BYTES = (OFF_XCH + XCH + 15) / 16 * 16;
   static constexpr int ALLOC = BYTES + 128;                   // slack to align the base to 128
   // byte offset of (row r, 16-byte chunk c) in a block's K or V codes: the chunks of rows 64 or 32 bytes long are
@@ -121,10 +122,12 @@ __device__ __forceinline__ void stsm_x2_t(uint32_t addr, uint32_t a, uint32_t b)
 // Barrier over the CTA, with a vote.
 __device__ __forceinline__ bool bar_or(bool x) { return __syncthreads_or(x) != 0; }
 
-// All tiles of the CTA. WIDE: with a reference of X for each row where the V scales of a tile need it; without it such a
-// tile is left wrong, and the return value asks the CTA for a second pass that has it. (One pass for both is slower
-// where no tile needs it, as the hot loop is out of registers: 32 requests of 4096 tokens 42.2 -> 43.2 us, 16 query rows a KV
-// head 105 -> 113. The second pass costs its CTAs the time once more, twice where every tile is wide: 44 -> 91 -> 123.)
+// All tiles of the CTA. WIDE: with a reference of X for each row where the V scales of a tile need it, with queries of
+// 2^104 and more, and with differences of scores taken before their factor where S and m are so large that their roundings
+// differ. Without it such a tile is left wrong, and the return value asks the CTA for a second pass that has it. (One
+// pass for both is slower where no tile needs it, as the hot loop is out of registers: 32 requests of 4096 tokens 42.2 ->
+// 43.2 us, 16 query rows a KV head 105 -> 113. The second pass costs its CTAs the time once more, twice where every tile
+// is wide: 44 -> 91 -> 123.)
 template <int D, int NQ, bool WIDE>
 __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
   using C = I4Cfg<D, NQ>;
@@ -137,8 +140,8 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
   Unit* queue = reinterpret_cast<Unit*>(sm + C::OFF_QUEUE);
   float* xmax = reinterpret_cast<float*>(sm + C::OFF_XCH);  // [warp][8 NQ]
   float* xsum = xmax + W * 8 * NQ;                          // [l, zero points][8 NQ][warp]
-  float* qrow = xsum + W * 2 * 8 * NQ;                      // [score factor, <1, q>, one over the factor][8 NQ]
-  int* xexp = reinterpret_cast<int*>(qrow + 3 * 8 * NQ);    // [largest, least][warp]
+  float* qrow = xsum + W * 2 * 8 * NQ;                      // [score factor, <1, q>, one over the factor, 2^32 or 1][8 NQ]
+  int* xexp = reinterpret_cast<int*>(qrow + 4 * 8 * NQ);    // [largest, least][warp]
   int* n_queued = xexp + 2 * W;                             // [2]: of every other refill
   int* redo = n_queued + 2;                                 // a second pass is needed
   float* xtop = reinterpret_cast<float*>(redo + 1);            // [8 NQ][warp]: of a wide tile, the largest X as an exponent
@@ -334,7 +337,8 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
         amax = max(amax & 0xffffu, amax >> 16);
         #pragma unroll
         for (int k = 1; k < LPQ; k <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, k));
-        const int E = amax == 0 ? 0 : min(max(14 + 127 - (int)(amax >> 7), -100), 100);
+        // largest element in [2^14, 2^15); below 2^-106 less, where 2^120 leaves every bf16 number exact all the same
+        const int E = amax == 0 ? 0 : min(14 + 127 - (int)(amax >> 7), 120);
         const float up = __int_as_float((127 + E) << 23);
         float v[8] = {bf16_lo(qx[i].x), bf16_hi(qx[i].x), bf16_lo(qx[i].y), bf16_hi(qx[i].y),
                       bf16_lo(qx[i].z), bf16_hi(qx[i].z), bf16_lo(qx[i].w), bf16_hi(qx[i].w)};
@@ -350,7 +354,10 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
         #pragma unroll
         for (int k = 1; k < LPQ; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
         if (sg == 0) {  // a row that is not finite has NaN scores where it sees a key; the mask comes after them
-          const float f = amax >= 0x7f80u ? 1.f : __int_as_float((127 + 24 - E) << 23) * p.qk_scale_log2;
+          const bool big = E < -90 && amax < 0x7f80u;  // 2^(24 - E) would leave fp32's range: 2^32 of it go to mask_block()
+          const float f = amax >= 0x7f80u ? 1.f : __int_as_float((127 + (big ? -8 : 24) - E) << 23) * p.qk_scale_log2;
+          if constexpr (WIDE) qrow[24 * NQ + row] = big ? 0x1p32f : 1.f;
+          else if (big) *redo = 1;
           qrow[row] = f;
           qrow[8 * NQ + row] = amax >= 0x7f80u ? __int_as_float(0x7fc00000) : sum * 0x1p-24f;
           qrow[16 * NQ + row] = 1.f / f;
@@ -372,6 +379,7 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
     int eref = 16;
     uint32_t slow = 0, swin = 0;
     bool wide = false;
+    [[maybe_unused]] float ref[NQ][2];  // WIDE: the references m as scores before their factor
     #pragma unroll
     for (int nw = 0; nw < NQ; ++nw)
       #pragma unroll
@@ -381,10 +389,19 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
         #pragma unroll
         for (int i = 0; i < 4; ++i) o[nw][e][i] = 0.f;
         thr[nw][e] = -INFINITY;
+        if constexpr (WIDE) ref[nw][e] = -INFINITY;
         nmu[nw][e] = lrow[nw][e] = zrow[nw][e] = 0.f;
       }
     // key j is visible to query token t if j <= Lb - T + t: keys below this need no mask in any row
-    const int safe_end = min(d.tok_end, d.seq_len - p.T + r0 / p.G + 1);
+    int safe_end = min(d.tok_end, d.seq_len - p.T + r0 / p.G + 1);
+    if constexpr (WIDE) {  // a row with a factor for mask_block() has it called in every block
+      bool big = false;
+      #pragma unroll
+      for (int nw = 0; nw < NQ; ++nw)
+        #pragma unroll
+        for (int e = 0; e < 2; ++e) big |= qrow[24 * NQ + 8 * nw + 2 * tig + e] != 1.f;
+      if (__any_sync(0xffffffffu, big)) safe_end = -kI4Block;
+    }
 
     // O^T += V^T X^T over the 64 keys at a place of the V ring, X in buffer xs
     auto product = [&](uint32_t place, int xs) {
@@ -478,6 +495,7 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
             const int r = r0 + 8 * nw + 2 * tig + (i & 1), j = j0 + (i >> 1) * 8;
             if (j >= d.tok_end || (r < p.GT && j > d.seq_len - p.T + r / p.G)) sv[mt][nw][i] = -INFINITY;
             else if (bad) sv[mt][nw][i] = __int_as_float(0x7fc00000);
+            else if (WIDE) sv[mt][nw][i] *= qrow[24 * NQ + 8 * nw + 2 * tig + (i & 1)];
           }
         }
         #pragma unroll
@@ -502,6 +520,7 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
       cp_async_wait<kI4Stages - 2>();
       return bar_or(over);
     };
+    [[maybe_unused]] auto less_ref = [&](float x, int nw, int e) { return x - (ref[nw][e] == -INFINITY ? 0.f : ref[nw][e]); };
     // New references: the exact maxima of the rows; of X from the first block's scales, or row by row.
     auto new_references = [&](bool first) {
       #pragma unroll
@@ -556,15 +575,26 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
         slow = eref == 16 ? 0u : (uint32_t)(eref - kI4Window) << 23;  // below 2^-111 there is nothing to lose
         swin = ((uint32_t)(eref + 1) << 23) - slow;
       }
-      if (!wide && (e_lo < (int)(slow >> 23) || e_hi > eref)) {
-        if constexpr (WIDE) {
+      bool far = e_lo < (int)(slow >> 23) || e_hi > eref;
+      [[maybe_unused]] float rold[NQ][2];
+      if constexpr (WIDE) {
+        #pragma unroll
+        for (int nw = 0; nw < NQ; ++nw)
+          #pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            rold[nw][e] = ref[nw][e];
+            #pragma unroll
+            for (int i = 0; i < W; ++i) ref[nw][e] = fmaxf(ref[nw][e], xmax[i * 8 * NQ + 8 * nw + 2 * tig + e]);
+            far |= ref[nw][e] != -INFINITY && fabsf(ref[nw][e] * fcol[nw][e]) >= kI4Far;
+          }
+        if (!wide && __any_sync(0xffffffffu, far)) {  // the same in every warp
           wide = true;
           swin = 0;  // every vote asks for new references
-        } else {
-          *redo = 1;
         }
+      } else {
+        if (far) *redo = 1;
       }
-      [[maybe_unused]] float mx2[NQ][2];  // largest s^V 2^S of the rows, as an exponent
+      [[maybe_unused]] float mx2[NQ][2];  // largest X of the rows, as an exponent
       if (WIDE && wide) {
         #pragma unroll
         for (int nw = 0; nw < NQ; ++nw)
@@ -575,7 +605,7 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
             for (int mt = 0; mt < MT; ++mt)
               #pragma unroll
               for (int k = 0; k < 2; ++k)
-                mx = fmaxf(mx, fmaf(sv[mt][nw][2 * k + e], fcol[nw][e], (float)(__float_as_int(vsc[mt][k]) >> 23 & 0xff)));
+                mx = fmaxf(mx, fmaf(less_ref(sv[mt][nw][2 * k + e], nw, e), fcol[nw][e], (float)(__float_as_int(vsc[mt][k]) >> 23 & 0xff)));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -602,16 +632,20 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
           const float mold = thr[nw][e] == -INFINITY ? -INFINITY : -nmu[nw][e];
           const float mnew = fmaxf(mold, mx * fcol[nw][e]);  // the factor is positive
           const float mu = mnew == -INFINITY ? 0.f : mnew;
-          const float alpha = fast_exp2(mold - mu);
+          float down = mold - mu;
+          if (WIDE && wide && mold != -INFINITY)
+            down = was_wide ? (rold[nw][e] - ref[nw][e]) * fcol[nw][e] : -fmaf(ref[nw][e], fcol[nw][e], -mold);
+          const float alpha = fast_exp2(down);
           float a = alpha;
           if (WIDE && wide) {
             const int eold = was_wide ? xrow[col] : eref;
-            const float top = fmaxf(mold + (float)eold, mx2[nw][e]) - mu;  // exponent of the largest X so far
+            const float top = fmaxf(down + (float)eold, mx2[nw][e]);  // exponent of the largest X so far
             const int enew = top > 16.f ? (int)ceilf(fminf(top, 254.f)) : 16;
-            a = fast_exp2(mold - mu + (float)(eold - enew));
+            a = fast_exp2(down + (float)(eold - enew));
             __syncwarp();  // all lanes have the old one
             if (gid == 0) xrow[col] = enew;
           }
+          if (!WIDE && mnew != -INFINITY && fabsf(mnew) >= kI4Far) *redo = 1;
           nmu[nw][e] = -mu;
           thr[nw][e] = mnew == -INFINITY ? -INFINITY : (mnew + (float)kI4Tau) * qrow[16 * NQ + col];
           lrow[nw][e] *= alpha;
@@ -665,7 +699,7 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
             const uint32_t sb = __float_as_uint(vsc[mt][i >> 1]);
             const int ev = max((int)(sb >> 23 & 0xff), 1);
             const float sig = (sb & 0x7f800000u) == 0 ? vsc[mt][i >> 1] * 0x1p126f : __uint_as_float((sb & 0x807fffffu) | 0x3f800000u);
-            const float t = fmaf(sv[mt][nw][i], fcol[nw][i & 1], nmu[nw][i & 1]);
+            const float t = less_ref(sv[mt][nw][i], nw, i & 1) * fcol[nw][i & 1];
             lrow[nw][i & 1] += fast_exp2(t);
             x[i] = fast_exp2(t + (float)(ev - xrow[8 * nw + 2 * tig + (i & 1)] + kI4XExp)) * sig;
           }

@@ -177,3 +177,42 @@ def test_a_query_row_that_is_not_finite_stays_alone(bad):
                                 nan[b, t, h] = False
                                 assert np.all(got[0][b, t, h] == 0) and np.isneginf(got[1][b, t, h])
         assert np.isnan(got[0][nan]).all() and np.isnan(got[1][nan]).all()
+
+
+@pytest.mark.parametrize("tile", [64, 512])
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_of_any_magnitude(d, tile):
+    """Keys small enough that the scores of the largest rows are ordinary numbers; rows of every magnitude side by
+    side."""
+    cache = I4.Cache([300, 70], Hkv=2, d=d, P=16, seed=116)
+    w = cache.words[0].astype(np.int64)
+    small = w - (120 << 7)                                   # K scales about 2^-122
+    cache.words[0] = np.where((w >> 7 & 255) > 120, small, w).astype(np.uint16)
+    q = np.random.default_rng(117).standard_normal((2, 2, 16, d))
+    q *= 2.0 ** np.array([123, 119, 116, 115, 110, 0, -40, -130, 122, 120, 117, 116, 100, 60, -80, -125])[:, None]
+    q = I4.bf16(q)
+    assert np.isfinite(q).all() and np.abs(q).max() > 2.0 ** 123
+    out, lse = _decode(cache, q, 2, tile=tile)
+    _check_decode(cache, q, 2, out, lse)
+
+
+def test_large_queries_over_ordinary_keys():
+    """Scores of 2^100 and more: the weights are those of the largest score, and finite."""
+    cache = I4.Cache([200], Hkv=1, d=128, P=16, seed=118)
+    q = np.random.default_rng(119).standard_normal((1, 1, 4, 128)) * 2.0 ** np.array([100, 113, 116, 118])[:, None]
+    q = I4.bf16(q)
+    out, lse = _decode(cache, q, 1, tile=256)
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    _check_decode(cache, q, 1, out, lse)
+
+
+@pytest.mark.parametrize("qs,ks", [(2.0 ** -125, 2.0 ** 121), (2.0 ** -110, 2.0 ** 110), (2.0 ** -90, 2.0 ** 88)])
+def test_small_queries_over_large_keys(qs, ks):
+    cache = I4.Cache([300], Hkv=1, d=128, P=16, seed=120)
+    k = int(np.log2(ks))
+    for i, pid in enumerate(cache.table[0]):
+        used = min(16, 300 - 16 * i)
+        cache.words[0, pid, :, :used] += k << 7
+    q = I4.bf16(np.random.default_rng(121).standard_normal((1, 1, 4, 128)) * qs)
+    out, lse = _decode(cache, q, 1, tile=64)
+    _check_decode(cache, q, 1, out, lse)
