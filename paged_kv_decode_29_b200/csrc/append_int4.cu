@@ -88,9 +88,11 @@ __device__ __forceinline__ uint32_t a4_quantise(const float (&x)[N], int (&c)[N]
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     ok &= __shfl_xor_sync(0xffffffffu, ok, o);
   }
-  const float h = 0.5f * hi - 0.5f * lo;  // half the range: hi - lo itself may pass fp32
-  uint32_t sb = __float_as_uint(h / 7.5f) & 0xfff00000u;
-  if (7.5f * __uint_as_float(sb) < h) sb += 0x00100000u;
+  // half the range, as hi - lo itself may pass fp32; where the sum is rounded, s must cover what it was: 7.5 s and the larger
+  // half have eight significant bits each and lie within a factor of 4, so their difference is exact
+  const float far = fmaxf(0.5f * hi, -0.5f * lo), near = fminf(0.5f * hi, -0.5f * lo);
+  uint32_t sb = __float_as_uint((far + near) / 7.5f) & 0xfff00000u;
+  if (7.5f * __uint_as_float(sb) - far < near) sb += 0x00100000u;
   sb = max(sb, 0x00800000u);  // 2^-126
   const float s = __uint_as_float(sb), r = 1.f / s;
   const int z = a4_code(-lo, r);

@@ -1,10 +1,12 @@
 """The INT4 cache at the ends of its numbers: V rows whose scales lie far apart, channels of zeros, NaN rows, queries of
 any magnitude, and the quantiser's scale where the range of a row is no fp32 number."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 
 from tests import _int4 as I4
-from tests.test_int4_gpu import _check_decode, _decode, _prefill
+from tests.test_int4_gpu import _append_case, _check_decode, _decode, _prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -216,3 +218,37 @@ def test_small_queries_over_large_keys(qs, ks):
     q = I4.bf16(np.random.default_rng(121).standard_normal((1, 1, 4, 128)) * qs)
     out, lse = _decode(cache, q, 1, tile=64)
     _check_decode(cache, q, 1, out, lse)
+
+
+# ---------------------------------------------------------------------------- the quantiser's scale
+def _quantise_row_exactly(x):
+    """I4.quantise_row in rational numbers (a float64 difference rounds where the ends lie 2^53 apart)."""
+    F = [Fraction(float(v)) for v in x]
+    lo, hi = min(Fraction(0), *F), max(Fraction(0), *F)
+    m, e = 8, -129                                           # m 2^e: from 2^-126 on
+    while 15 * m * Fraction(2) ** e < hi - lo:
+        m, e = (m + 1, e) if m < 15 else (8, e + 1)
+    s = m * Fraction(2) ** e
+    z = round(-lo / s)                                       # ties to even
+    return np.array([min(15, max(0, round(v / s) + z)) for v in F]), float(s), z
+
+
+def test_the_scale_covers_the_range_exactly(monkeypatch):
+    """Rows whose hi - lo is no fp32 number: 15 s = hi and a lo below hi's last place make the next larger scale the
+    smallest one that covers the range."""
+    rng = np.random.default_rng(123)
+    for _ in range(50):                                      # the two oracles agree where both are exact
+        x = I4.bf16(rng.standard_normal(64) * 2.0 ** rng.integers(-20, 20))
+        for a, b in zip(I4.quantise_row(x), _quantise_row_exactly(x)):
+            assert np.array_equal(a, b)
+    monkeypatch.setattr(I4, "quantise_row", _quantise_row_exactly)
+
+    def edit(q, k, v):
+        for i, (hi, lo) in enumerate([(15.0, -2.0 ** -21), (15.0, -2.0 ** -40), (2.0 ** -21, -15.0), (2.0 ** -100, -15.0),
+                                      (15.0, -2.0 ** -133), (15.0 * 2.0 ** 100, -1.0), (120.0, -2.0 ** -16), (8.0, -2.0 ** -30),
+                                      (15.0 * 2.0 ** -126, -2.0 ** -133)]):
+            v[i] = 0.0
+            v[i, 0, 0], v[i, 0, 9], v[i, 1, 64], v[i, 1, 65] = hi, lo, lo, hi
+    _append_case([60, 61], [5, 5], hq=4, hkv=2, d=128, P=16, packed=True, seed=122, edit=edit)
+    _, s, z = I4.quantise_row([15.0, -2.0 ** -21])
+    assert s == 1.125 and z == 0
