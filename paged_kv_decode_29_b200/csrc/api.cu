@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "host_errors.h"
+#include "int4.cuh"
 
 namespace decattn {
 
@@ -224,7 +225,7 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
     if (!int4 && (!make_kv_map(&tmK, k_pages, s.kv_dtype, D, rows) || !make_kv_map(&tmV, v_pages, s.kv_dtype, D, rows)))
       return cuda_fail("K/V tensor map (cuTensorMapEncodeTiled)");
     const float scale = s.sm_scale > 0.f ? s.sm_scale : 1.0f / sqrtf((float)D);
-    SplitParams sp;
+    SplitInt4Params sp;
     sp.q = static_cast<const uint16_t*>(q);
     sp.page_table = page_table;
     sp.seq_lens = seq_lens;
@@ -249,7 +250,7 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
     if (e != cudaSuccess) return cuda_fail("split kernel launch", e);
   }
   if (stages & kStageCombine) {
-    CombineParams cp;
+    CombineBf16Params cp;
     cp.plan = static_cast<const char*>(plan->buf);
     cp.seq_lens = seq_lens;
     cp.part_o = part_o;
@@ -262,7 +263,8 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
     cp.B = s.batch; cp.T = s.q_tokens; cp.Hq = s.n_q_heads; cp.Hkv = s.n_kv_heads; cp.G = G; cp.GT = GT; cp.D = D;
     cp.tl = plan->tile_len;
     cp.sparse = plan->sparse;
-    if (const cudaError_t e = launch_combine(cp, dev, st); e != cudaSuccess) return cuda_fail("combine kernel launch", e);
+    const cudaError_t e = int4 ? launch_combine_bf16(cp, dev, st) : launch_combine(cp, dev, st);
+    if (e != cudaSuccess) return cuda_fail("combine kernel launch", e);
   }
   return DECATTN_OK;
 }
@@ -304,7 +306,7 @@ static int prefill_enqueue(const dec_attn_shape* shape, const void* q, const voi
     return cuda_fail("prefill tensor maps (cuTensorMapEncodeTiled)");
   if (splits <= 1) tmP = tmO;  // not used
   const float scale = s.sm_scale > 0.f ? s.sm_scale : 1.0f / sqrtf((float)s.head_dim);
-  PrefillParams p;
+  PrefillPartsParams p;
   p.q = static_cast<const uint16_t*>(q);
   p.page_table = page_table;
   p.seq_lens = seq_lens;
@@ -325,7 +327,8 @@ static int prefill_enqueue(const dec_attn_shape* shape, const void* q, const voi
   if (expand)
     if (const cudaError_t e = launch_widen_int4(*expand, static_cast<cudaStream_t>(stream)); e != cudaSuccess)
       return cuda_fail("INT4 prefill expansion launch", e);
-  const cudaError_t e = launch_prefill(p, tmQ, tmK, tmV, tmO, tmP, static_cast<cudaStream_t>(stream));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = bf16_out ? launch_prefill_parts(p, tmQ, tmK, tmV, tmO, tmP, st) : launch_prefill(p, tmQ, tmK, tmV, tmO, st);
   return e == cudaSuccess ? DECATTN_OK : cuda_fail("prefill kernel launch", e);
 }
 

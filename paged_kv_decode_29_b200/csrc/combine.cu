@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "int4.cuh"
 
 namespace decattn {
 
@@ -39,15 +40,17 @@ struct CombineVec {
 
 // BF16: the row is written to p.out_bf16, rounded once, and a NaN weight (a NaN row of an INT4 cache) is
 // passed on; the fp32 output takes such a row for an empty one.
+template <bool BF16>
+using CombineArgs = std::conditional_t<BF16, CombineBf16Params, CombineParams>;
 template <int D, bool BF16>
-__device__ __forceinline__ void write_row(const CombineParams& p, int64_t row, int lane, float M, float W,
+__device__ __forceinline__ void write_row(const CombineArgs<BF16>& p, int64_t row, int lane, float M, float W,
                                           const float (&acc)[D / 32]) {
   constexpr int VEC = D / 32;
   using V = typename CombineVec<D>::T;
   float* lse_out = p.lse + row;
   const bool empty = BF16 ? W == 0.f : (M == -INFINITY || !(W > 0.f));
   const float inv = empty ? 0.f : 1.f / W;
-  if (BF16) {
+  if constexpr (BF16) {
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.out_bf16 + row * D) + lane * (VEC / 2);
     #pragma unroll
     for (int e = 0; e < VEC; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
@@ -64,7 +67,7 @@ __device__ __forceinline__ void write_row(const CombineParams& p, int64_t row, i
 // Items are numbered unit by unit: per request (dense plans: every KV head of a request has the
 // same tiles) or per (request, KV head) pair (block-sparse plans); NU units of RPU query rows.
 template <int D, bool SPARSE, bool BF16>
-__global__ void __launch_bounds__(kCombineThreads, kCombineCtasPerSm) combine_kernel(const CombineParams p) {
+__global__ void __launch_bounds__(kCombineThreads, kCombineCtasPerSm) combine_kernel(const CombineArgs<BF16> p) {
   constexpr int VEC = D / 32;
   using V = typename CombineVec<D>::T;
   extern __shared__ int32_t req_sm[];  // chunk prefix [NU + 1], tile prefix [NU + 1], seq_lens [B + 1]
@@ -258,17 +261,14 @@ __global__ void __launch_bounds__(kCombineThreads, kCombineCtasPerSm) combine_ke
   }
 }
 
-cudaError_t launch_combine(const CombineParams& p, int device, cudaStream_t st) {
+template <bool BF16>
+static cudaError_t launch(const CombineArgs<BF16>& p, int device, cudaStream_t st) {
   if ((int64_t)p.B * p.T * p.Hq <= 0) return cudaSuccess;
   const int sms = default_bins(device) / split_ctas_per_sm();
   if (sms <= 0) return cudaErrorUnknown;
   if (p.D != 128 && p.D != 64) return cudaErrorInvalidValue;
-  auto pick = [&](auto bf16) -> const void* {
-    constexpr bool BF = decltype(bf16)::value;
-    return p.sparse ? (p.D == 128 ? (const void*)combine_kernel<128, true, BF> : (const void*)combine_kernel<64, true, BF>)
-                    : (p.D == 128 ? (const void*)combine_kernel<128, false, BF> : (const void*)combine_kernel<64, false, BF>);
-  };
-  const void* fn = p.out_bf16 ? pick(std::true_type{}) : pick(std::false_type{});
+  const void* fn = p.sparse ? (p.D == 128 ? (const void*)combine_kernel<128, true, BF16> : (const void*)combine_kernel<64, true, BF16>)
+                            : (p.D == 128 ? (const void*)combine_kernel<128, false, BF16> : (const void*)combine_kernel<64, false, BF16>);
   const int64_t nu = p.sparse ? (int64_t)p.B * p.Hkv : p.B;
   const int smem = nu <= kCombineSmemRequests ? (int)(4 * (2 * (nu + 1) + p.B + 1)) : 0;
   if (smem > 48 * 1024 && !ensure_smem_attr(fn, smem)) return cudaErrorInvalidValue;
@@ -282,8 +282,11 @@ cudaError_t launch_combine(const CombineParams& p, int device, cudaStream_t st) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  void* args[] = {const_cast<CombineParams*>(&p)};
+  void* args[] = {const_cast<CombineArgs<BF16>*>(&p)};
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
+
+cudaError_t launch_combine(const CombineParams& p, int device, cudaStream_t st) { return launch<false>(p, device, st); }
+cudaError_t launch_combine_bf16(const CombineBf16Params& p, int device, cudaStream_t st) { return launch<true>(p, device, st); }
 
 }  // namespace decattn

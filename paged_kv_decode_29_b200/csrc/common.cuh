@@ -177,11 +177,6 @@ struct SplitParams {
   float qk_scale_log2;      // sm_scale * log2(e)
   uint64_t wait_ns;         // a pipeline wait gives up after this long (kWaitLimitNs unless a test lowers it)
   int32_t skip_fill;        // tests only: CTA 0's producer leaves this ring fill out (-1: none)
-  // INT4 cache (int4.cuh) only:
-  const uint8_t* k_codes;   // [num_pages][Hkv][P][D / 2]
-  const uint8_t* v_codes;
-  const uint16_t* kv_words; // row words [2][num_pages][Hkv][P]
-  uint16_t* out_bf16;       // bf16 [B][T][Hq][D], in place of out
 };
 
 // Arguments of the prefill kernel (prefill.cu). Query rows are packed: request b's Tb rows are
@@ -194,7 +189,6 @@ struct PrefillParams {
   const int32_t* seq_lens;    // [B]
   const int32_t* cu_q;        // [B + 1] row offsets, or null
   float* out;                 // [total_rows][Hq][D]
-  uint16_t* out_bf16;         // bf16 output in place of out (null: fp32)
   float* lse;                 // [total_rows][Hq]
   int32_t* status;            // optional device word
   int B, T, Hq, Hkv, G, P, num_pages, mpps;
@@ -202,18 +196,7 @@ struct PrefillParams {
   float qk_scale_log2;        // sm_scale * log2(e)
   uint64_t wait_ns;           // a pipeline wait gives up after this long
   int32_t skip_fill;          // tests only: CTA 0's producer leaves this K block out (-1: none)
-  // bf16 output only: the keys of a request are split over up to `splits` CTAs (prefill_splits)
-  int splits;
-  float* part_o;              // [splits][total_rows][Hq][D] normalised partials
-  float* part_lse;            // [splits][total_rows][Hq]
 };
-
-// Key blocks of 128 that one CTA of a split prefill takes of a request with Lb keys; a row block that sees n
-// key blocks has ceil(n / that) parts. Short requests are split less: a part has two blocks at least.
-__host__ __device__ inline int prefill_part_blocks(int Lb, int splits) {
-  const int n = (Lb + 127) / 128, per = (n + splits - 1) / splits;
-  return per < 2 ? 2 : per;
-}
 
 // FP8 prefill: the E4M3 pages each request uses, widened to a bf16 scratch pool (prefill_fp8.cu).
 struct WidenParams {
@@ -227,20 +210,6 @@ struct WidenParams {
   int32_t* pt_out;            // [B][mpps]: b * mpps + i
   int32_t* status;            // optional device word
   int B, Hkv, P, D, num_pages, mpps;
-};
-
-// INT4 prefill: the pages each request uses, expanded to a bf16 scratch pool (prefill_int4.cu).
-struct WidenInt4Params {
-  const uint8_t* k_codes;     // [num_pages][Hkv][P][D / 2]
-  const uint8_t* v_codes;
-  const uint16_t* kv_words;   // [2][num_pages][Hkv][P]: K, then V
-  const int32_t* page_table;  // [B][mpps]
-  const int32_t* seq_lens;    // [B]
-  uint16_t* k_out;            // bf16 [B * mpps][Hkv][P][D]: page i of request b at b * mpps + i
-  uint16_t* v_out;
-  int32_t* pt_out;            // [B][mpps]: b * mpps + i
-  int32_t* status;            // optional device word
-  int B, Hkv, P, num_pages, mpps;
 };
 
 // Query rows of one KV head that a decode tile computes at once (G * T), and query tokens per
@@ -269,7 +238,6 @@ struct CombineParams {
   float* chunk_state;       // [items][D + 4]: max, weight, -, -, then the weighted sum
   int B, T, Hq, Hkv, G, GT, D, tl;
   int sparse;               // block-sparse plan: chunks are counted per (request, KV head) pair
-  uint16_t* out_bf16;       // INT4 cache: bf16 output in place of out (null: fp32)
 };
 
 __host__ __device__ inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -516,16 +484,11 @@ int split_ctas_per_sm();                                          // split.cu
 bool split_tc_supported(int kv_dtype, int D, int GT);             // split_tc.cu
 cudaError_t launch_split_tc(const SplitParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, int kv_dtype,
                             cudaStream_t st);                     // split_tc.cu
-bool split_int4_supported(int D, int GT);                         // split_int4.cu
-cudaError_t launch_split_int4(const SplitParams& p, int D, int device, cudaStream_t st);  // split_int4.cu
 cudaError_t launch_combine(const CombineParams& p, int device, cudaStream_t st);  // combine.cu
 cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
-                           const CUtensorMap& tmV, const CUtensorMap& tmO, const CUtensorMap& tmP,
-                           cudaStream_t st);                      // prefill.cu
-int prefill_splits(int B, int T, int Hq, int G, int64_t max_keys);  // prefill.cu
+                           const CUtensorMap& tmV, const CUtensorMap& tmO, cudaStream_t st);  // prefill.cu
 // bytes of the widened pool (K, then V at *off_v, then the page table at *off_pt)   prefill_fp8.cu
 int64_t widen_scratch_bytes(int B, int mpps, int Hkv, int P, int D, int64_t* off_v, int64_t* off_pt);
 cudaError_t launch_widen_kv(const WidenParams& p, cudaStream_t st);  // prefill_fp8.cu
-cudaError_t launch_widen_int4(const WidenInt4Params& p, cudaStream_t st);  // prefill_int4.cu
 
 }  // namespace decattn

@@ -1,5 +1,5 @@
-// int4.cuh -- the INT4 cache format (DECATTN_KV_INT4) and its decoding, shared by the append, decode
-// and prefill kernels.
+// int4.cuh -- the INT4 cache format (DECATTN_KV_INT4): its decoding, shared by the append, decode and prefill kernels,
+// and the launches over it.
 //
 // A row is the head_dim elements of one (page, KV head, slot) of K or V: head_dim / 2 bytes of codes,
 // element 2 i in the low and 2 i + 1 in the high four bits of byte i, and one 16-bit word: the word
@@ -44,5 +44,56 @@ __device__ __forceinline__ uint4 int4_to_bf16(uint32_t x, uint32_t word) {
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
+
+// ------------------------------------------------------------------ launches
+// The split kernel over an INT4 cache (split_int4.cu): out_bf16 in place of out.
+struct SplitInt4Params : SplitParams {
+  const uint8_t* k_codes;   // [num_pages][Hkv][P][D / 2]
+  const uint8_t* v_codes;
+  const uint16_t* kv_words; // row words [2][num_pages][Hkv][P]
+  uint16_t* out_bf16;       // bf16 [B][T][Hq][D]
+};
+bool split_int4_supported(int D, int GT);                         // split_int4.cu
+cudaError_t launch_split_int4(const SplitInt4Params& p, int D, int device, cudaStream_t st);  // split_int4.cu
+
+// The combine kernel with a bf16 output in place of out.
+struct CombineBf16Params : CombineParams {
+  uint16_t* out_bf16;
+};
+cudaError_t launch_combine_bf16(const CombineBf16Params& p, int device, cudaStream_t st);  // combine.cu
+
+// The pages each request uses, expanded to a bf16 scratch pool (prefill_int4.cu).
+struct WidenInt4Params {
+  const uint8_t* k_codes;     // [num_pages][Hkv][P][D / 2]
+  const uint8_t* v_codes;
+  const uint16_t* kv_words;   // [2][num_pages][Hkv][P]: K, then V
+  const int32_t* page_table;  // [B][mpps]
+  const int32_t* seq_lens;    // [B]
+  uint16_t* k_out;            // bf16 [B * mpps][Hkv][P][D]: page i of request b at b * mpps + i
+  uint16_t* v_out;
+  int32_t* pt_out;            // [B][mpps]: b * mpps + i
+  int32_t* status;            // optional device word
+  int B, Hkv, P, num_pages, mpps;
+};
+cudaError_t launch_widen_int4(const WidenInt4Params& p, cudaStream_t st);  // prefill_int4.cu
+
+// The prefill kernel with a bf16 output in place of out, the keys of a request split over up to `splits` CTAs.
+struct PrefillPartsParams : PrefillParams {
+  uint16_t* out_bf16;         // bf16 [total_rows][Hq][D]
+  int splits;                 // prefill_splits
+  float* part_o;              // [splits][total_rows][Hq][D] normalised partials
+  float* part_lse;            // [splits][total_rows][Hq]
+};
+
+// Key blocks of 128 that one CTA of a split prefill takes of a request with Lb keys; a row block that sees n
+// key blocks has ceil(n / that) parts. Short requests are split less: a part has two blocks at least.
+__host__ __device__ inline int prefill_part_blocks(int Lb, int splits) {
+  const int n = (Lb + 127) / 128, per = (n + splits - 1) / splits;
+  return per < 2 ? 2 : per;
+}
+int prefill_splits(int B, int T, int Hq, int G, int64_t max_keys);  // prefill.cu
+cudaError_t launch_prefill_parts(const PrefillPartsParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                 const CUtensorMap& tmV, const CUtensorMap& tmO, const CUtensorMap& tmP,
+                                 cudaStream_t st);                // prefill.cu
 
 }  // namespace decattn

@@ -20,7 +20,10 @@
 // first, then separate K and V rings of two 128-key stages), 9 MMA issue (one thread). The
 // epilogue stages O through the Q area and writes it with TMA stores. Every wait is bounded
 // (DECATTN_ETIMEOUT, then an orderly exit).
+#include <type_traits>
+
 #include "common.cuh"
+#include "int4.cuh"
 #include "tc.cuh"
 
 namespace decattn {
@@ -159,8 +162,10 @@ __device__ __forceinline__ void pf_bulk_wait_all() { asm volatile("cp.async.bulk
 // over p.splits CTAs (numbered between the row-block step and the request), whose fp32 parts
 // prefill_combine_kernel merges; otherwise out is fp32 and nothing is split.
 template <bool BF16OUT>
+using PfArgs = std::conditional_t<BF16OUT, PrefillPartsParams, PrefillParams>;
+template <bool BF16OUT>
 __global__ void __launch_bounds__(kPfThreads, 1)
-prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+prefill_kernel(const PfArgs<BF16OUT> p, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                const __grid_constant__ CUtensorMap tmP) {
   using L = PfSmem;
@@ -178,7 +183,8 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
   const bool head_pair = (p.G % 2) == 0;
   const int ny = head_pair ? p.Hq / 2 : p.Hq;
   const int nsteps = head_pair ? pf_tiles_per_head(p.T) : (pf_tiles_per_head(p.T) + 1) / 2;
-  const int nsplit = BF16OUT ? p.splits : 1;
+  int nsplit = 1;
+  if constexpr (BF16OUT) nsplit = p.splits;
   int step = nsteps - 1 - (int)blockIdx.x / (p.B * ny * nsplit);
   int split = (int)blockIdx.x / (p.B * ny) % nsplit;
   int b = (int)blockIdx.x % (p.B * ny) / ny;
@@ -507,8 +513,15 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
       const int parts = u ? parts1 : parts0;
       const bool part = BF16OUT && parts > 1;  // one of several: fp32, rows behind those of the parts before
       const int64_t prow = part ? (int64_t)split * p.total_rows : 0;
-      float* const out_f = part ? p.part_o : p.out;
-      float* const lse_f = part ? p.part_lse : p.lse;
+      float *out_f = p.out, *lse_f = p.lse;
+      [[maybe_unused]] uint16_t* out_h = nullptr;
+      if constexpr (BF16OUT) {
+        out_h = p.out_bf16;
+        if (part) {
+          out_f = p.part_o;
+          lse_f = p.part_lse;
+        }
+      }
       if (split >= parts) {
         // this tile has no such part
       } else if (BF16OUT && !part) {
@@ -530,7 +543,7 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmQ, c
           }
           if (!whole_box) {
             if (t < Tb) {
-              uint4* dst = reinterpret_cast<uint4*>(p.out_bf16 + ((int64_t)(qoff + t) * p.Hq + qh) * kPfD + 64 * q2);
+              uint4* dst = reinterpret_cast<uint4*>(out_h + ((int64_t)(qoff + t) * p.Hq + qh) * kPfD + 64 * q2);
               #pragma unroll
               for (int c = 0; c < 8; ++c) dst[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
             }
@@ -605,7 +618,7 @@ constexpr int kPfcThreads = 256;
 constexpr int kPfcAhead = 4;     // parts whose loads are in flight (a divisor of kPfMaxParts)
 constexpr int kPfMaxParts = 32;  // a lane of the combine each
 
-__global__ void __launch_bounds__(kPfcThreads) prefill_combine_kernel(const PrefillParams p) {
+__global__ void __launch_bounds__(kPfcThreads) prefill_combine_kernel(const PrefillPartsParams p) {
   griddep_wait();
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * (kPfcThreads / 32) + (threadIdx.x >> 5);
@@ -677,13 +690,16 @@ int prefill_splits(int B, int T, int Hq, int G, int64_t max_keys) {
   return (int)(n < most ? n : most < 1 ? 1 : most);
 }
 
-cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
-                           const CUtensorMap& tmV, const CUtensorMap& tmO, const CUtensorMap& tmP, cudaStream_t st) {
+template <bool BF16OUT>
+static cudaError_t launch(const PfArgs<BF16OUT>& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                          const CUtensorMap& tmV, const CUtensorMap& tmO, const CUtensorMap& tmP, cudaStream_t st) {
   const int smem = PfSmem::ALLOC;
-  const auto fn = p.out_bf16 ? prefill_kernel<true> : prefill_kernel<false>;
+  const auto fn = prefill_kernel<BF16OUT>;
+  int splits = 1;
+  if constexpr (BF16OUT) splits = p.splits;
   if (!ensure_smem_attr((const void*)fn, smem)) return cudaErrorInvalidValue;
   if (p.B == 0 || p.T == 0 || p.Hq == 0) return cudaSuccess;
-  const int64_t grid = (int64_t)pf_grid(p.B, p.T, p.Hq, p.G) * (p.out_bf16 ? p.splits : 1);
+  const int64_t grid = (int64_t)pf_grid(p.B, p.T, p.Hq, p.G) * splits;
   if (grid <= 0 || grid > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -694,14 +710,28 @@ cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tmQ, const
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see griddep_wait in the kernels
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.out_bf16 ? 1 : 0;
+  cfg.numAttrs = BF16OUT ? 1 : 0;
   if (const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p, tmQ, tmK, tmV, tmO, tmP); e != cudaSuccess) return e;
-  if (!p.out_bf16 || p.splits == 1) return cudaSuccess;
-  const int64_t items = p.total_rows * p.Hq;
-  cfg.gridDim = dim3((unsigned)((items + kPfcThreads / 32 - 1) / (kPfcThreads / 32)));
-  cfg.blockDim = dim3(kPfcThreads);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, prefill_combine_kernel, p);
+  if constexpr (BF16OUT) {
+    if (splits == 1) return cudaSuccess;
+    const int64_t items = p.total_rows * p.Hq;
+    cfg.gridDim = dim3((unsigned)((items + kPfcThreads / 32 - 1) / (kPfcThreads / 32)));
+    cfg.blockDim = dim3(kPfcThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, prefill_combine_kernel, p);
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                           const CUtensorMap& tmV, const CUtensorMap& tmO, cudaStream_t st) {
+  return launch<false>(p, tmQ, tmK, tmV, tmO, tmO, st);
+}
+
+cudaError_t launch_prefill_parts(const PrefillPartsParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                 const CUtensorMap& tmV, const CUtensorMap& tmO, const CUtensorMap& tmP,
+                                 cudaStream_t st) {
+  return launch<true>(p, tmQ, tmK, tmV, tmO, tmP, st);
 }
 
 }  // namespace decattn

@@ -129,7 +129,7 @@ __device__ __forceinline__ bool bar_or(bool x) { return __syncthreads_or(x) != 0
 // 43.2 us, 16 query rows a KV head 105 -> 113. The second pass costs its CTAs the time once more, twice where every tile
 // is wide: 44 -> 91 -> 123.)
 template <int D, int NQ, bool WIDE>
-__device__ __forceinline__ bool i4_pass(const SplitParams& p) {
+__device__ __forceinline__ bool i4_pass(const SplitInt4Params& p) {
   using C = I4Cfg<D, NQ>;
   constexpr int W = C::W, MT = C::MT;
   extern __shared__ uint8_t smem_raw[];
@@ -389,7 +389,7 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
         #pragma unroll
         for (int i = 0; i < 4; ++i) o[nw][e][i] = 0.f;
         thr[nw][e] = -INFINITY;
-        if constexpr (WIDE) ref[nw][e] = -INFINITY;
+        ref[nw][e] = -INFINITY;
         nmu[nw][e] = lrow[nw][e] = zrow[nw][e] = 0.f;
       }
     // key j is visible to query token t if j <= Lb - T + t: keys below this need no mask in any row
@@ -794,14 +794,14 @@ __device__ __forceinline__ bool i4_pass(const SplitParams& p) {
 }
 
 template <int D, int NQ>
-__device__ __noinline__ void i4_wide_pass(const SplitParams& p) {
+__device__ __noinline__ void i4_wide_pass(const SplitInt4Params& p) {
   __syncthreads();  // the first pass is done with the shared memory
   i4_pass<D, NQ, true>(p);
 }
 
 template <int D, int NQ, int CPS>
 __global__ void __launch_bounds__(I4Cfg<D, NQ>::THREADS, CPS)
-split_int4_kernel(const __grid_constant__ SplitParams p) {
+split_int4_kernel(const __grid_constant__ SplitInt4Params p) {
   // Everything below reads or writes what earlier kernels of the stream may still be working on: the
   // plan, the pages (a plan serves every layer of a step, so the kernel before this one can be the
   // append), the combine counters.
@@ -815,7 +815,7 @@ split_int4_kernel(const __grid_constant__ SplitParams p) {
 
 // ------------------------------------------------------------------ host side
 template <int D, int NQ, int CPS>
-static cudaError_t launch_i4(const SplitParams& p, int sms, cudaStream_t st) {
+static cudaError_t launch_i4(const SplitInt4Params& p, int sms, cudaStream_t st) {
   using C = I4Cfg<D, NQ>;
   static_assert(CPS * (C::ALLOC + 1024) <= 228 * 1024, "the CTAs fit an SM's shared memory");
   auto fn = split_int4_kernel<D, NQ, CPS>;
@@ -836,14 +836,14 @@ static cudaError_t launch_i4(const SplitParams& p, int sms, cudaStream_t st) {
 }
 
 template <int D>
-static cudaError_t launch_i4_gt(const SplitParams& p, int sms, cudaStream_t st) {
+static cudaError_t launch_i4_gt(const SplitInt4Params& p, int sms, cudaStream_t st) {
   constexpr int CPS = D == 64 ? 8 : 4;
   return p.GT <= 8 ? launch_i4<D, 1, CPS>(p, sms, st) : launch_i4<D, 2, CPS>(p, sms, st);
 }
 
 bool split_int4_supported(int D, int GT) { return GT >= 1 && GT <= kMaxGT && (D == 64 || D == 128); }
 
-cudaError_t launch_split_int4(const SplitParams& p, int D, int device, cudaStream_t st) {
+cudaError_t launch_split_int4(const SplitInt4Params& p, int D, int device, cudaStream_t st) {
   if (!split_int4_supported(D, p.GT)) return cudaErrorInvalidValue;
   const int sms = default_bins(device) / split_ctas_per_sm();
   if (sms <= 0) return cudaErrorUnknown;
