@@ -498,7 +498,8 @@ DECATTN_API int dec_attn_run_int4(const dec_attn_shape *shape, const void *q, co
                                   size_t workspace_bytes, void *out, float *lse, void *stream);
 
 /* Workspace bytes of dec_attn_prefill_int4 for this shape (batch, q_tokens, heads and pages count), negative on an
- * error. */
+ * error. Two bf16 pools of batch * max_pages_per_seq pages: the lengths are on the device, so a table that is wider
+ * than the longest request needs costs memory here (not time in the call); pass one that is cut to it. */
 DECATTN_API int64_t dec_attn_prefill_int4_workspace_bytes(const dec_attn_shape *shape);
 
 /* Causal prefill over an INT4 cache (shape->kv_dtype DECATTN_KV_INT4, head_dim 128, page_size a multiple of

@@ -612,14 +612,21 @@ def run_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_w
 
 def prefill_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_words: torch.Tensor,
                  page_table: torch.Tensor, seq_lens: torch.Tensor, *, cu_q_lens: torch.Tensor | None = None,
-                 max_q_rows: int = 0, sm_scale: float = 0.0, workspace: torch.Tensor | None = None,
-                 out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-                 status: torch.Tensor | None = None, stream=None):
+                 max_q_rows: int = 0, max_kv_len: int | None = None, sm_scale: float = 0.0,
+                 workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 lse: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
     """dec_attn_prefill_int4: causal prefill over an INT4 cache; returns (out bf16, lse fp32) shaped like q's
     rows. q is bf16 [B][T][Hq][128] (cu_q_lens None) or packed [total][Hq][128] with cu_q_lens int32 [B + 1] and
     ``max_q_rows`` bounding every request's rows. ``workspace``: uint8 device buffer of at least
-    prefill_int4_workspace_bytes (allocated here if None)."""
+    prefill_int4_workspace_bytes (allocated here if None). It grows with the width of page_table: where that is much wider
+    than the longest request needs, give ``max_kv_len``, a bound on seq_lens (a longer request is reported in ``status``);
+    the columns past it are then left out."""
     lib = _lib or load_library()
+    if max_kv_len is not None:
+        width = _int4_table_width(k_pages, page_table, max_kv_len)
+        if width < page_table.shape[1]:
+            with torch.cuda.stream(_other_stream(stream, page_table.device)):
+                page_table = page_table[:, :width].contiguous()
     shape, total, dev = _int4_args(q, k_pages, v_pages, kv_words, page_table, seq_lens, cu_q_lens, workspace, out, lse, status=status)
     shape.sm_scale = sm_scale
     if cu_q_lens is not None:
@@ -640,12 +647,23 @@ def prefill_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     return out, lse
 
 
-def prefill_int4_workspace_bytes(q_shape, k_pages: torch.Tensor, page_table: torch.Tensor, max_q_rows: int = 0) -> int:
+def _int4_table_width(k_pages: torch.Tensor, page_table: torch.Tensor, max_kv_len: int | None) -> int:
+    """Columns of the table that a call with this bound on seq_lens looks at."""
+    if max_kv_len is None:
+        return page_table.shape[1]
+    if max_kv_len < 0:
+        raise ValueError("max_kv_len is a number of keys")
+    return min(page_table.shape[1], max(-(-int(max_kv_len) // k_pages.shape[2]), 1))
+
+
+def prefill_int4_workspace_bytes(q_shape, k_pages: torch.Tensor, page_table: torch.Tensor, max_q_rows: int = 0,
+                                 max_kv_len: int | None = None) -> int:
     """dec_attn_prefill_int4_workspace_bytes for q of this shape ([B][T][Hq][128], or packed [total][Hq][128] with
-    ``max_q_rows``) and these pools."""
+    ``max_q_rows``), these pools and this bound on seq_lens."""
     num_pages, Hkv, P, half = k_pages.shape
+    width = _int4_table_width(k_pages, page_table, max_kv_len)
     T = int(q_shape[1]) if len(q_shape) == 4 else int(max_q_rows)
-    shape = ShapeT(page_table.shape[0], int(q_shape[-2]), Hkv, 2 * half, T, P, num_pages, page_table.shape[1], KV_INT4, 0.0)
+    shape = ShapeT(page_table.shape[0], int(q_shape[-2]), Hkv, 2 * half, T, P, num_pages, width, KV_INT4, 0.0)
     n = int(load_library().dec_attn_prefill_int4_workspace_bytes(C.byref(shape)))
     if n < 0:
         raise DecAttnError(n, "dec_attn_prefill_int4_workspace_bytes")

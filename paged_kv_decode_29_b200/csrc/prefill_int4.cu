@@ -20,29 +20,20 @@ namespace decattn {
 
 constexpr int kWiThreads = 128;
 constexpr int kWiD = 128;
+constexpr int kWiPerSm = 16;  // CTAs that a multiprocessor holds: 2048 threads
+constexpr int kWiWaves = 4;
 constexpr int kWiBatch = 4;  // 16-byte outputs of K and of V that a thread has in flight
 
-// CTA (w, h): scratch page w = b * mpps + i (page i of request b), KV head h, K and V. A thread takes
-// 8 codes (4 bytes) of a row at a time and writes 16 bytes, so a warp reads two rows' codes (128 bytes)
-// and writes 512 bytes in a row. Pages past the request's keys are never read by the prefill kernel and
-// are left unwritten; the rows past its last key, up to a multiple of 16, are zero. A page id outside
-// the pool is reported (DECATTN_EDEVICE) and its scratch page is zero.
-__global__ void __launch_bounds__(kWiThreads) widen_int4_kernel(const WidenInt4Params p) {
-  griddep_wait();               // the pages were written by earlier kernels of the stream
-  griddep_launch_dependents();  // the prefill kernel may be scheduled; it waits for this grid itself
-  const int w = (int)blockIdx.x, h = (int)blockIdx.y;
-  const int b = w / p.mpps, i = w - b * p.mpps;
+// Scratch page w, which holds keys first .. of a request with Lb keys, of KV head h. A thread takes 8 codes (4 bytes)
+// of a row at a time and writes 16 bytes, so a warp reads two rows' codes (128 bytes) and writes 512 bytes in a
+// row. The rows past the last key, up to a multiple of 16, are zero. A page id outside the pool is reported
+// (DECATTN_EDEVICE) and its scratch page is zero.
+__device__ __forceinline__ void widen_page(const WidenInt4Params& p, int w, int h, int first, int Lb) {
   if (threadIdx.x == 0 && h == 0) p.pt_out[w] = w;
-  const int Lb = p.seq_lens[b];
-  if (Lb < 0) {
-    if (threadIdx.x == 0 && i == 0 && h == 0) set_status(p.status, DECATTN_EDEVICE);
-    return;
-  }
-  if ((int64_t)i * p.P >= Lb) return;
   const int pid = p.page_table[w];
   const bool good = pid >= 0 && pid < p.num_pages;
   if (!good && threadIdx.x == 0 && h == 0) set_status(p.status, DECATTN_EDEVICE);
-  const int rows = min(p.P, (int)(Lb - i * p.P));  // rows of the page that hold a key
+  const int rows = min(p.P, Lb - first);  // rows of the page that hold a key
   const int64_t src = ((int64_t)(good ? pid : 0) * p.Hkv + h) * p.P;
   const int64_t dst = ((int64_t)w * p.Hkv + h) * p.P;
   const uint16_t* kw = p.kv_words + src;
@@ -76,12 +67,33 @@ __global__ void __launch_bounds__(kWiThreads) widen_int4_kernel(const WidenInt4P
   }
 }
 
+// CTA (x, h, b): pages x, x + gridDim.x, .. of request b, KV head h, K and V; page i goes to scratch page
+// b * mpps + i. Pages past the request's keys are never read by the prefill kernel and are left unwritten.
+__global__ void __launch_bounds__(kWiThreads) widen_int4_kernel(const WidenInt4Params p) {
+  griddep_wait();               // the pages were written by earlier kernels of the stream
+  griddep_launch_dependents();  // the prefill kernel may be scheduled; it waits for this grid itself
+  const int h = (int)blockIdx.y, b = (int)blockIdx.z;
+  const int Lb = p.seq_lens[b];
+  if (Lb < 0 && threadIdx.x == 0 && blockIdx.x == 0 && h == 0) set_status(p.status, DECATTN_EDEVICE);
+  for (int i = (int)blockIdx.x; i < p.mpps && (int64_t)i * p.P < Lb; i += (int)gridDim.x)
+    widen_page(p, b * p.mpps + i, h, i * p.P, Lb);
+}
+
 cudaError_t launch_widen_int4(const WidenInt4Params& p, cudaStream_t st) {
-  const int64_t grid = (int64_t)p.B * p.mpps;
-  if (grid <= 0) return cudaSuccess;
-  if (grid > 0x7fffffff || p.Hkv > 65535) return cudaErrorInvalidValue;
+  if (p.B <= 0 || p.mpps <= 0) return cudaSuccess;
+  if (p.Hkv > 65535 || p.B > 65535) return cudaErrorInvalidValue;
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  const int sms = default_bins(dev) / split_ctas_per_sm();
+  // A CTA a page, as the table allows for them, up to kWiWaves full GPUs: the host does not know the lengths, and
+  // a server's table is as wide as its longest context may become. 5 chunks of 1 to 219 pages, 5 KV heads, all three
+  // kernels: 83 us with a table of 219 pages, 86 with one of 4096 (181 with a CTA for each of its pages).
+  const int64_t rows = (int64_t)p.B * p.Hkv, most = (int64_t)kWiWaves * kWiPerSm * sms;
+  int64_t x = (most + rows - 1) / rows;
+  if (x > p.mpps) x = p.mpps;
+  if (x < 1) x = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)p.Hkv);
+  cfg.gridDim = dim3((unsigned)x, (unsigned)p.Hkv, (unsigned)p.B);
   cfg.blockDim = dim3(kWiThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
