@@ -502,6 +502,11 @@ DECATTN_API int dec_attn_run_int4(const dec_attn_shape *shape, const void *q, co
  * than the longest request needs costs memory here (not time in the call); pass one that is cut to it. */
 DECATTN_API int64_t dec_attn_prefill_int4_workspace_bytes(const dec_attn_shape *shape);
 
+/* The same for a packed call with total_q_rows rows, never less. A batch whose requests have few of their q_tokens rows
+ * (one chunk among single rows) leaves CTAs free, for which dec_attn_prefill_int4 splits the keys further where
+ * the workspace has room for the parts: this much has it. */
+DECATTN_API int64_t dec_attn_prefill_int4_packed_workspace_bytes(const dec_attn_shape *shape, int64_t total_q_rows);
+
 /* Causal prefill over an INT4 cache (shape->kv_dtype DECATTN_KV_INT4, head_dim 128, page_size a multiple of
  * 16): the pages of the requests are expanded into `workspace` as a bf16 pool (exact) and the bf16 prefill
  * kernel runs on it. Arguments as dec_attn_prefill_fp8 with kv_words (16-byte aligned, like codes and

@@ -31,7 +31,8 @@ API = ("dec_attn_default_bins", "dec_attn_default_tile_len", "dec_attn_plan_byte
        "dec_attn_read_status", "dec_attn_status_string", "dec_attn_append_rope", "dec_attn_append_rope_fp8", "dec_attn_prefill",
        "dec_attn_prefill_varlen", "dec_attn_prefill_fp8_workspace_bytes", "dec_attn_prefill_fp8",
        "dec_attn_plan_sparse_bytes",
-       "dec_attn_append_rope_int4", "dec_attn_run_int4", "dec_attn_prefill_int4_workspace_bytes", "dec_attn_prefill_int4",
+       "dec_attn_append_rope_int4", "dec_attn_run_int4", "dec_attn_prefill_int4_workspace_bytes",
+       "dec_attn_prefill_int4_packed_workspace_bytes", "dec_attn_prefill_int4",
        "dec_attn_plan_sparse", "dec_attn_last_error", "dec_attn_test_set_waits")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -123,6 +124,8 @@ def load_library(path: str = LIB_PATH):
         lib.dec_attn_run_int4.restype = i32
         lib.dec_attn_prefill_int4_workspace_bytes.argtypes = [C.POINTER(ShapeT)]
         lib.dec_attn_prefill_int4_workspace_bytes.restype = i64
+        lib.dec_attn_prefill_int4_packed_workspace_bytes.argtypes = [C.POINTER(ShapeT), i64]
+        lib.dec_attn_prefill_int4_packed_workspace_bytes.restype = i64
         lib.dec_attn_prefill_int4.argtypes = [C.POINTER(ShapeT), vp, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp, vp]
         lib.dec_attn_prefill_int4.restype = i32
         lib.dec_attn_test_set_waits.argtypes = [C.c_uint64, C.c_int32]
@@ -634,9 +637,7 @@ def prefill_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     out = _int4_result("out", out, q.shape, _BF16, q, stream)
     lse = _int4_result("lse", lse, q.shape[:-1], torch.float32, q, stream)
     if workspace is None:
-        need = lib.dec_attn_prefill_int4_workspace_bytes(C.byref(shape))
-        if need < 0:
-            raise DecAttnError(need, "dec_attn_prefill_int4_workspace_bytes")
+        need = _int4_prefill_bytes(shape, None if cu_q_lens is None else total)
         workspace = _new(max(need, 16), torch.uint8, q.device, stream, result=False)
     rc = lib.dec_attn_prefill_int4(C.byref(shape), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_words.data_ptr(),
                                    page_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_q_lens), total, workspace.data_ptr(),
@@ -658,13 +659,19 @@ def _int4_table_width(k_pages: torch.Tensor, page_table: torch.Tensor, max_kv_le
 
 def prefill_int4_workspace_bytes(q_shape, k_pages: torch.Tensor, page_table: torch.Tensor, max_q_rows: int = 0,
                                  max_kv_len: int | None = None) -> int:
-    """dec_attn_prefill_int4_workspace_bytes for q of this shape ([B][T][Hq][128], or packed [total][Hq][128] with
-    ``max_q_rows``), these pools and this bound on seq_lens."""
+    """dec_attn_prefill_int4_workspace_bytes for q of this shape ([B][T][Hq][128]; for packed [total][Hq][128] with
+    ``max_q_rows``, dec_attn_prefill_int4_packed_workspace_bytes), these pools and this bound on seq_lens."""
     num_pages, Hkv, P, half = k_pages.shape
     width = _int4_table_width(k_pages, page_table, max_kv_len)
     T = int(q_shape[1]) if len(q_shape) == 4 else int(max_q_rows)
     shape = ShapeT(page_table.shape[0], int(q_shape[-2]), Hkv, 2 * half, T, P, num_pages, width, KV_INT4, 0.0)
-    n = int(load_library().dec_attn_prefill_int4_workspace_bytes(C.byref(shape)))
+    return _int4_prefill_bytes(shape, int(q_shape[0]) if len(q_shape) == 3 else None)
+
+
+def _int4_prefill_bytes(shape: ShapeT, packed_rows: int | None) -> int:
+    lib = load_library()
+    n = int(lib.dec_attn_prefill_int4_workspace_bytes(C.byref(shape)) if packed_rows is None else
+            lib.dec_attn_prefill_int4_packed_workspace_bytes(C.byref(shape), packed_rows))
     if n < 0:
         raise DecAttnError(n, "dec_attn_prefill_int4_workspace_bytes")
     return n

@@ -319,6 +319,8 @@ static int prefill_enqueue(const dec_attn_shape* shape, const void* q, const voi
   p.P = s.page_size; p.num_pages = s.num_pages; p.mpps = s.max_pages_per_seq;
   p.total_rows = total_rows;
   p.splits = splits > 0 ? splits : 1;
+  const int64_t items = prefill_items(s.batch, s.q_tokens, p.G, total_rows);
+  p.items = cu_q && items < prefill_items(s.batch, s.q_tokens, p.G, (int64_t)s.batch * s.q_tokens) ? (int)items : 0;
   p.part_o = parts;
   p.part_lse = parts ? parts + p.splits * total_rows * s.n_q_heads * s.head_dim : nullptr;
   p.qk_scale_log2 = scale * 1.4426950408889634f;
@@ -381,13 +383,13 @@ static int prefill_fp8_enqueue(const dec_attn_shape* shape, const void* q, const
 }
 
 // Workspace of the INT4 prefill: the expanded pools and their page table (widen_scratch_bytes), then, where the
-// keys are split, the parts of batch * q_tokens rows (fp32 out and lse).
-static int64_t prefill_int4_scratch(const dec_attn_shape& s, int64_t* off_v, int64_t* off_pt, int64_t* off_parts, int* splits) {
+// keys are split, the parts of that many rows (fp32 out and lse).
+static int64_t prefill_int4_scratch(const dec_attn_shape& s, int64_t rows, int64_t* off_v, int64_t* off_pt, int64_t* off_parts,
+                                    int* splits) {
   const int64_t wide =
       widen_scratch_bytes(s.batch, s.max_pages_per_seq, s.n_kv_heads, s.page_size, s.head_dim, off_v, off_pt);
-  const int64_t rows = (int64_t)s.batch * s.q_tokens;
-  const int n = rows > 0 ? prefill_splits(s.batch, s.q_tokens, s.n_q_heads, s.n_q_heads / s.n_kv_heads,
-                                        (int64_t)s.max_pages_per_seq * s.page_size) : 1;
+  const int n = rows > 0 ? prefill_splits(s.batch, s.q_tokens, s.n_q_heads, s.n_q_heads / s.n_kv_heads, rows,
+                                          (int64_t)s.max_pages_per_seq * s.page_size) : 1;
   if (off_parts) *off_parts = wide;
   if (splits) *splits = n;
   return wide + (n > 1 ? align_up(n * rows * s.n_q_heads * (s.head_dim + 1) * 4, 256) : 0);
@@ -418,8 +420,13 @@ static int prefill_int4_enqueue(const dec_attn_shape* shape, const void* q, cons
     return DECATTN_EALIGN;
   int64_t off_v = 0, off_pt = 0, off_parts = 0;
   int splits = 1;
-  const int64_t need = prefill_int4_scratch(s, &off_v, &off_pt, &off_parts, &splits);
-  if (workspace_bytes < need) return DECATTN_ESMALL;
+  if (workspace_bytes < prefill_int4_scratch(s, (int64_t)s.batch * s.q_tokens, &off_v, &off_pt, &off_parts, &splits))
+    return DECATTN_ESMALL;
+  if (cu_q) {  // as many parts as the rows that there are ask for and the workspace has room for
+    prefill_int4_scratch(s, total_rows, nullptr, nullptr, nullptr, &splits);
+    const int64_t room = (workspace_bytes - off_parts) / (total_rows * s.n_q_heads * (s.head_dim + 1) * 4);
+    if (splits > room) splits = room < 1 ? 1 : (int)room;
+  }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* parts = splits > 1 ? reinterpret_cast<float*>(ws + off_parts) : nullptr;
   dec_attn_shape wide = s;  // the expanded pool: bf16, page i of request b at b * max_pages_per_seq + i
@@ -452,7 +459,16 @@ extern "C" int64_t dec_attn_prefill_int4_workspace_bytes(const dec_attn_shape* s
   if (s.batch < 0 || s.n_kv_heads <= 0 || s.page_size <= 0 || s.max_pages_per_seq < 0 || s.head_dim <= 0 ||
       s.n_q_heads <= 0 || s.n_q_heads % s.n_kv_heads != 0 || s.q_tokens <= 0)
     return DECATTN_EINVAL;
-  return prefill_int4_scratch(s, nullptr, nullptr, nullptr, nullptr);
+  return prefill_int4_scratch(s, (int64_t)s.batch * s.q_tokens, nullptr, nullptr, nullptr, nullptr);
+}
+
+extern "C" int64_t dec_attn_prefill_int4_packed_workspace_bytes(const dec_attn_shape* shape, int64_t total_q_rows) {
+  const int64_t least = dec_attn_prefill_int4_workspace_bytes(shape);
+  if (least < 0) return least;
+  if (total_q_rows < 0) return DECATTN_EINVAL;
+  const int64_t most = (int64_t)shape->batch * shape->q_tokens;
+  const int64_t bytes = prefill_int4_scratch(*shape, total_q_rows < most ? total_q_rows : most, nullptr, nullptr, nullptr, nullptr);
+  return bytes > least ? bytes : least;
 }
 
 extern "C" int dec_attn_prefill_int4(const dec_attn_shape* shape, const void* q, const void* k_pages,

@@ -81,6 +81,7 @@ cudaError_t launch_widen_int4(const WidenInt4Params& p, cudaStream_t st);  // pr
 struct PrefillPartsParams : PrefillParams {
   uint16_t* out_bf16;         // bf16 [total_rows][Hq][D]
   int splits;                 // prefill_splits
+  int items;                  // packed rows: row-block steps in the grid (prefill_items); 0: every request has as many
   float* part_o;              // [splits][total_rows][Hq][D] normalised partials
   float* part_lse;            // [splits][total_rows][Hq]
 };
@@ -91,7 +92,10 @@ __host__ __device__ inline int prefill_part_blocks(int Lb, int splits) {
   const int n = (Lb + 127) / 128, per = (n + splits - 1) / splits;
   return per < 2 ? 2 : per;
 }
-int prefill_splits(int B, int T, int Hq, int G, int64_t max_keys);  // prefill.cu
+// Row-block steps (a CTA each, per head or pair of heads and part) that B requests of up to T rows can come to with
+// total_rows rows in all, and the parts that their keys are split into.   prefill.cu
+int64_t prefill_items(int B, int T, int G, int64_t total_rows);
+int prefill_splits(int B, int T, int Hq, int G, int64_t total_rows, int64_t max_keys);
 cudaError_t launch_prefill_parts(const PrefillPartsParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                  const CUtensorMap& tmV, const CUtensorMap& tmO, const CUtensorMap& tmP,
                                  cudaStream_t st);                // prefill.cu

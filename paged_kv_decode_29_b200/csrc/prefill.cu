@@ -189,7 +189,54 @@ prefill_kernel(const PfArgs<BF16OUT> p, const __grid_constant__ CUtensorMap tmQ,
   int split = (int)blockIdx.x / (p.B * ny) % nsplit;
   int b = (int)blockIdx.x % (p.B * ny) / ny;
   const int y = (int)blockIdx.x % ny;
-  if (BF16OUT && nsplit > 1 && p.B <= 32) {
+  int items = 0;
+  if constexpr (BF16OUT) items = p.items;
+  if (BF16OUT && items > 0) {
+    // packed rows that fill a part of the B x nsteps grid only: the CTAs are numbered through the steps that there are
+    // (every warp finds its own way, from the offsets)
+    const int i = (int)blockIdx.x / ny, it = i / nsplit, step_rows = head_pair ? kPfM : 2 * kPfM;
+    split = i % nsplit;
+    // the steps of request r, 0 for one that is past the last or whose offsets lie outside the packed rows (reported)
+    auto steps_of = [&](int r) {
+      if (r >= p.B) return 0;
+      const int c0 = p.cu_q[r], c1 = p.cu_q[r + 1];
+      if (c0 < 0 || c1 < c0 || c1 - c0 > p.T || (int64_t)c1 > p.total_rows) {
+        set_status(p.status, DECATTN_EDEVICE);
+        return 0;
+      }
+      return (c1 - c0 + step_rows - 1) / step_rows;
+    };
+    int at = 0, n = 0;  // steps before this lane's request, and its own
+    if (p.B <= 32) {    // the longest request first, as below
+      n = steps_of(lane);
+      const int len = lane < p.B ? p.seq_lens[lane] : 0;
+      for (int j = 0; j < p.B; ++j) {
+        const int lj = __shfl_sync(0xffffffffu, len, j), nj = __shfl_sync(0xffffffffu, n, j);
+        at += lj > len || (lj == len && j < lane) ? nj : 0;
+      }
+      b = lane;
+    } else {
+      int total = 0;
+      for (b = lane; b - lane < p.B; b += 32) {
+        n = steps_of(b);
+        at = n;
+        #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, at, o);
+          at += lane >= o ? x : 0;
+        }
+        const int upto = total + __shfl_sync(0xffffffffu, at, 31);
+        at += total - n;
+        if (it < upto) break;
+        total = upto;
+      }
+    }
+    const unsigned has = __ballot_sync(0xffffffffu, it >= at && it < at + n);
+    if (has == 0) return;  // fewer steps than the host allows for
+    const int from = __ffs(has) - 1;
+    b = __shfl_sync(0xffffffffu, b, from);
+    step = __shfl_sync(0xffffffffu, at + n, from) - 1 - it;  // its steps counted down
+  } else if (BF16OUT && nsplit > 1 && p.B <= 32) {
     // a small grid of requests of unequal length: the longest request's CTAs first, all of its parts (5 ragged chunks:
     // 103.8 us in the order above, 94.0 in this one). The lengths are ranked by one warp, so up to 32 requests.
     const int i = (int)blockIdx.x / ny;
@@ -676,16 +723,28 @@ __global__ void __launch_bounds__(kPfcThreads) prefill_combine_kernel(const Pref
   if (lane == 0) p.lse[item] = W == 0.f ? -INFINITY : M + logf(W);
 }
 
-// Parts that the keys are split into at most, and no more than a request with max_keys keys can have. A small grid
-// becomes one wave of a B200's 148 multiprocessors (a CTA fills one, and its start and end cost as much as four key
-// blocks); a larger one up to four waves, whose parts differ in length (the heaviest come first, short ones
-// fill up), in four parts at most. 5 ragged chunks (a grid of 200): 134 us in one part, 90.5 in two, 89.6 in three,
-// 89.2 in four, 115 in eight. 106 rows over 9982 keys (a grid of 24): 40.9 us in 10 parts (two waves), 32.7 in six.
-int prefill_splits(int B, int T, int Hq, int G, int64_t max_keys) {
-  const int64_t grid = pf_grid(B, T, Hq, G);
+int64_t prefill_items(int B, int T, int G, int64_t total_rows) {
+  const int step_rows = G % 2 == 0 ? kPfM : 2 * kPfM;
+  const int64_t all = (int64_t)B * ((T + step_rows - 1) / step_rows), packed = total_rows / step_rows + B;
+  return packed < all ? packed : all;  // a request's last step is part full
+}
+
+// Parts that the keys are split into at most, and no more than a request with max_keys keys can have. A grid of half the
+// multiprocessors at most becomes one wave of them (a CTA fills one, and its start and end cost as much as four key
+// blocks); a larger one up to three waves, whose parts differ in length (the heaviest come first, short ones
+// fill up), in four parts at most. The grid is that of the rows there are. 106 rows over 9982 keys (a grid of 24): 40.9
+// us in 10 parts (two waves), 32.7 in six. 5 ragged chunks (a grid of 120, counted as 150): 134 us in one part, then two
+// waves 90.2, three 79.8, four 85.8; 4 chunks of 640 rows behind 5000 keys (a grid of 160): three 171, four 179; a
+// chunk of 512 and 31 single rows, 32 query heads: 572 in one part, three waves 467, four 505.
+int prefill_splits(int B, int T, int Hq, int G, int64_t total_rows, int64_t max_keys) {
+  const int64_t grid = prefill_items(B, T, G, total_rows) * (G % 2 == 0 ? Hq / 2 : Hq);
   if (grid <= 0) return 1;
-  int64_t n = grid <= 74 ? 148 / grid : (4 * 148 + grid - 1) / grid;
-  if (n > (grid <= 74 ? kPfMaxParts : 4)) n = grid <= 74 ? kPfMaxParts : 4;
+  int dev = 0;
+  int64_t sms = cudaGetDevice(&dev) == cudaSuccess ? default_bins(dev) / split_ctas_per_sm() : 0;
+  if (sms <= 0) sms = 148;  // asked for a size without a device
+  const bool small = 2 * grid <= sms;
+  int64_t n = small ? sms / grid : (3 * sms + grid - 1) / grid;
+  if (n > (small ? kPfMaxParts : 4)) n = small ? kPfMaxParts : 4;
   const int64_t most = (max_keys + 2 * kPfN - 1) / (2 * kPfN);  // prefill_part_blocks: two key blocks at least
   return (int)(n < most ? n : most < 1 ? 1 : most);
 }
@@ -699,7 +758,9 @@ static cudaError_t launch(const PfArgs<BF16OUT>& p, const CUtensorMap& tmQ, cons
   if constexpr (BF16OUT) splits = p.splits;
   if (!ensure_smem_attr((const void*)fn, smem)) return cudaErrorInvalidValue;
   if (p.B == 0 || p.T == 0 || p.Hq == 0) return cudaSuccess;
-  const int64_t grid = (int64_t)pf_grid(p.B, p.T, p.Hq, p.G) * splits;
+  int64_t grid = (int64_t)pf_grid(p.B, p.T, p.Hq, p.G) * splits;
+  if constexpr (BF16OUT)
+    if (p.items > 0) grid = (int64_t)p.items * (p.G % 2 == 0 ? p.Hq / 2 : p.Hq) * splits;
   if (grid <= 0 || grid > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
