@@ -673,14 +673,24 @@ __global__ void __launch_bounds__(kPfcThreads) prefill_combine_kernel(const Pref
   const int row = (int)(item / p.Hq);
   int b, c0, Tb;
   if (p.cu_q) {
-    if (row >= p.cu_q[p.B]) return;
-    int upto = 0;  // requests with cu_q[b] <= row: the last of them has the row (a split grid has few requests)
-    for (int i = lane; i - lane < p.B; i += 32) upto += __popc(__ballot_sync(0xffffffffu, i < p.B && p.cu_q[i] <= row));
-    if (upto == 0) return;
-    b = upto - 1;
+    // the request that has the row, among those whose CTAs ran: offsets outside the packed rows are reported, and take no
+    // other request's rows (a split grid has few requests)
+    b = -1;
+    for (int i = lane; i - lane < p.B; i += 32) {
+      bool has = false;
+      if (i < p.B) {
+        const int s0 = p.cu_q[i], s1 = p.cu_q[i + 1];
+        has = s0 >= 0 && row >= s0 && row < s1 && s1 - s0 <= p.T && (int64_t)s1 <= p.total_rows;
+      }
+      const unsigned who = __ballot_sync(0xffffffffu, has);
+      if (who) {
+        b = i - lane + __ffs(who) - 1;
+        break;
+      }
+    }
+    if (b < 0) return;  // behind the last request, or of none
     c0 = p.cu_q[b];
     Tb = p.cu_q[b + 1] - c0;
-    if (c0 < 0 || row < c0 || Tb > p.T || (int64_t)c0 + Tb > p.total_rows) return;  // reported, not written
   } else {
     b = row / p.T;
     c0 = b * p.T;
