@@ -4,7 +4,9 @@ from fractions import Fraction
 
 import numpy as np
 import pytest
+import torch
 
+import paged_kv_decode_29_b200 as da
 from tests import _int4 as I4
 from tests.test_int4_gpu import _append_case, _check_decode, _decode, _prefill
 
@@ -252,3 +254,66 @@ def test_the_scale_covers_the_range_exactly(monkeypatch):
     _append_case([60, 61], [5, 5], hq=4, hkv=2, d=128, P=16, packed=True, seed=122, edit=edit)
     _, s, z = I4.quantise_row([15.0, -2.0 ** -21])
     assert s == 1.125 and z == 0
+
+
+# ---------------------------------------------------------------------------- second passes
+def _spread(cache, seed, span):
+    """V scales times powers of two of their own."""
+    rng = np.random.default_rng(seed)
+    for b, n in enumerate(cache.lens):
+        for i, pid in enumerate(cache.table[b, :-(-n // cache.P)]):
+            used = min(cache.P, n - cache.P * i)
+            w = cache.words[1, pid, :, :used].astype(np.int64)
+            cache.words[1, pid, :, :used] = w + (rng.integers(-span, span + 1, w.shape) << 7)
+
+
+@pytest.mark.parametrize("n_bins", [1, 2, 5])
+@pytest.mark.parametrize("hq,T", [(8, 1), (16, 2), (24, 2)])
+def test_far_scales_in_many_short_tiles_of_few_bins(hq, T, n_bins):
+    """A CTA walks more tiles than it fetches descriptors for at a time, twice over."""
+    cache = I4.Cache([16 * 70, 0, 5, 16 * 33 + 1], Hkv=2, d=128, P=16, seed=171)
+    _spread(cache, 172, 40)
+    q = I4.bf16(np.random.default_rng(173).standard_normal((4, T, hq, 128)))
+    out, lse = _decode(cache, q, T, tile=16, n_bins=n_bins)
+    _check_decode(cache, q, T, out, lse)
+
+
+def test_far_scales_in_one_tile_of_a_ctas_many():
+    """The tiles that need no second pass come out as in the first."""
+    cache = I4.Cache([640, 300], Hkv=2, d=128, P=16, seed=174)
+    q = I4.bf16(np.random.default_rng(175).standard_normal((2, 2, 8, 128)))
+    ref = _decode(cache, q, 2, tile=64, n_bins=3)
+    _add_exponent(cache, 1, 0, 1, 300, 60)
+    out, lse = _decode(cache, q, 2, tile=64, n_bins=3)
+    _check_decode(cache, q, 2, out, lse)
+    assert np.array_equal(out[1], ref[0][1]) and np.array_equal(lse[1], ref[1][1])
+    assert np.array_equal(out[0, :, :4], ref[0][0, :, :4]) and np.array_equal(lse[0, :, :4], ref[1][0, :, :4])
+
+
+def test_far_scales_under_a_block_sparse_plan():
+    lens, tile = [900, 64, 0, 2000], 64
+    cache = I4.Cache(lens, Hkv=2, d=128, P=16, seed=176)
+    _spread(cache, 177, 30)
+    q = I4.bf16(np.random.default_rng(178).standard_normal((4, 2, 8, 128)))
+    bits = np.random.default_rng(179).random((4, 2, 32)) < 0.4
+    bits[0, 1] = False
+    mask = (bits.astype(np.uint64) << np.arange(32, dtype=np.uint64)).sum(-1).astype(np.uint32)
+    keep = np.repeat(bits, tile, axis=-1)
+    out, lse = _decode(cache, q, 2, tile=tile, mask=torch.from_numpy(mask.view(np.int32)[..., None].copy()).cuda())
+    _check_decode(cache, q, 2, out, lse, keep=[keep[b][:, :n] for b, n in enumerate(lens)])
+
+
+def test_far_scales_bad_pages_and_nan_rows_together():
+    cache = I4.Cache([500, 300], Hkv=1, d=64, P=16, seed=180)
+    _spread(cache, 181, 50)
+    q = I4.bf16(np.random.default_rng(182).standard_normal((2, 3, 4, 64)))
+    ref = _decode(cache, q, 3, tile=128)
+    _check_decode(cache, q, 3, *ref)
+    _set_row(cache, 1, 1, 0, 299, 0x7FC0)                    # seen by the last row alone
+    dev = cache.to_device()
+    dev["tab"][0, 5] = -1
+    out, lse = _decode(cache, q, 3, tile=128, dev=dev, expect=da.EDEVICE)
+    assert np.isnan(out[1, 2]).all() and np.isnan(lse[1, 2]).all()
+    cache.words[1, cache.table[1, 18], 0, 299 % 16] = 0x3F80
+    want = _decode(cache, q, 3, tile=128)
+    assert np.array_equal(out[1, :2], want[0][1, :2]) and np.array_equal(lse[1, :2], want[1][1, :2])
