@@ -8,15 +8,15 @@
 // The tensor cores see codes, untouched but for a mask: a code in bits 0 .. 3 or 4 .. 7 of a half-word is the f16
 // number c 2^-24 or c 2^-20 (a subnormal). Scales and zero points act on one score or one weight instead of on
 // head_dim elements.
-//  * q_r, of any magnitude, is scaled by a power of two per row, so that its eight significant bits are exact in f16 down to 2^-24
-//    of the row's largest element, and within 2^-35 of that below.
+//  * q_r, of any magnitude, is scaled by a power of two per row, so that its eight significant bits are exact in f16 down
+//    to 2^-24 of the row's largest element, and within 2^-35 of that below.
 //  * X is rounded once to f16, relative to a reference of m and of s^V (a power of two near the largest s^V
 //    is divided out, and put back at the end): off by at most 2^-11 of itself, an eighth of the rounding that the bf16
 //    output gets anyway, or by 2^-22 of the row's largest X. That holds while a tile's V scales lie within 2^kI4Window of
 //    one another; a tile with others has a reference of X for each row, the largest X that the row has seen, and new
 //    references in every block ("wide": the key whose scale is far out may have no weight, or be hidden from the row).
-//    Both sums of O take the rounded X, so a key's part of an element is off by that share of
-//    X (c - z), and a channel of zeros stays one. m, l, the zero points' sum, O and the partials are fp32.
+//    Both sums of O take the rounded X, so a key's part of an element is off by that share of X (c - z), and a
+//    channel of zeros stays one (but for the fp32 sums). m, l, the zero points' sum, O and the partials are fp32.
 //
 // CTA = W = head_dim / 32 warps, all alike. The KV stream is cut into blocks of 64 keys. Of every block warp w
 // copies keys 64 w / W .. into the rings, computes their scores, and of O holds head dims 32 w .. 32 w + 31 over
@@ -59,6 +59,7 @@ constexpr int kI4XExp = 9;     // X < 2^(kI4Tau + 1 + kI4XExp) = 2^15
 // all. The largest X of a row is then 2^(kI4XExp - kI4Window) at least, and f16's subnormal rounding 2^-25.
 constexpr int kI4Room = 4;
 constexpr int kI4Window = 12;
+constexpr int kI4Least = kI4XExp + 1;  // least exponent of X's reference: 2^(kI4Least - kI4XExp - 127) is a normal number
 constexpr float kI4Far = 0x1p20f;  // |m| from which S - m is taken the other way: here m is off by up to 2^-4, and P by 2^(2^-4)
 constexpr int kI4Queue = 64;   // tile descriptors at hand: 32 are fetched at a time
 
@@ -144,8 +145,8 @@ __device__ __forceinline__ bool i4_pass(const SplitInt4Params& p) {
   int* xexp = reinterpret_cast<int*>(qrow + 4 * 8 * NQ);    // [largest, least][warp]
   int* n_queued = xexp + 2 * W;                             // [2]: of every other refill
   int* redo = n_queued + 2;                                 // a second pass is needed
-  float* xtop = reinterpret_cast<float*>(redo + 1);            // [8 NQ][warp]: of a wide tile, the largest X as an exponent
-  int* xrow = redo + 1 + W * 8 * NQ + w * 8 * NQ;       // [warp][8 NQ]: of a wide tile, the references of X
+  float* xtop = reinterpret_cast<float*>(redo + 1);         // [8 NQ][warp]: of a wide tile, the largest X as an exponent
+  int* xrow = redo + 1 + W * 8 * NQ + w * 8 * NQ;           // [warp][8 NQ]: of a wide tile, the references of X
   if (threadIdx.x == 0) *redo = 0;  // many barriers before its first use
 
   // ======================================================================= tiles
@@ -376,7 +377,7 @@ __device__ __forceinline__ bool i4_pass(const SplitInt4Params& p) {
     float lrow[NQ][2], zrow[NQ][2];  // this lane's keys' shares of l and of the zero points' sum
     // X's reference is 2^(eref - 127), in a wide tile xrow's for each row; the scales that it serves have bit
     // patterns from slow up to slow + swin (a negative or NaN scale never has one)
-    int eref = 16;
+    int eref = kI4Least;
     uint32_t slow = 0, swin = 0;
     bool wide = false;
     [[maybe_unused]] float ref[NQ][2];  // WIDE: the references m as scores before their factor
@@ -571,8 +572,8 @@ __device__ __forceinline__ bool i4_pass(const SplitInt4Params& p) {
       }
       [[maybe_unused]] const bool was_wide = wide;
       if (first) {
-        eref = min(max(e_hi + kI4Room, 16), 254);
-        slow = eref == 16 ? 0u : (uint32_t)(eref - kI4Window) << 23;  // below 2^-111 there is nothing to lose
+        eref = min(max(e_hi + kI4Room, kI4Least), 254);
+        slow = (uint32_t)max(eref - kI4Window, 0) << 23;
         swin = ((uint32_t)(eref + 1) << 23) - slow;
       }
       bool far = e_lo < (int)(slow >> 23) || e_hi > eref;
@@ -640,7 +641,7 @@ __device__ __forceinline__ bool i4_pass(const SplitInt4Params& p) {
           if (WIDE && wide) {
             const int eold = was_wide ? xrow[col] : eref;
             const float top = fmaxf(down + (float)eold, mx2[nw][e]);  // exponent of the largest X so far
-            const int enew = top > 16.f ? (int)ceilf(fminf(top, 254.f)) : 16;
+            const int enew = top > (float)kI4Least ? (int)ceilf(fminf(top, 254.f)) : kI4Least;
             a = fast_exp2(down + (float)(eold - enew));
             __syncwarp();  // all lanes have the old one
             if (gid == 0) xrow[col] = enew;
@@ -772,7 +773,7 @@ __device__ __forceinline__ bool i4_pass(const SplitInt4Params& p) {
           z += xs[8 * NQ * W + i];
         }
         if (o_rows[nw][e] < 0) continue;
-        const float unref = __int_as_float(((WIDE && wide ? xrow[8 * nw + 2 * tig + e] : eref) - kI4XExp) << 23);  // 16 at least
+        const float unref = __int_as_float(((WIDE && wide ? xrow[8 * nw + 2 * tig + e] : eref) - kI4XExp) << 23);
         const float inv = l == 0.f ? 0.f : unref / l;
         const float lse_v = l == 0.f ? -INFINITY : (__log2f(l) - nmu[nw][e]) * LN2;
         const float v[4] = {fmaf(o[nw][0][e], 16777216.f, -z) * inv, fmaf(o[nw][0][e + 2], 1048576.f, -z) * inv,

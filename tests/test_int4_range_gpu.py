@@ -79,6 +79,25 @@ def test_v_scales_of_any_spread(hq, T, d, span):
         _check_decode(cache, q, T, out, lse, what=f"tile {tile}")
 
 
+@pytest.mark.parametrize("low,high", [(1, 4), (3, 12), (8, 20), (1, 60), (240, 250)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_v_scales_at_the_ends_of_their_range(low, high, d):
+    """Biased exponents low .. high."""
+    cache = I4.Cache([130, 700], Hkv=2, d=d, P=16, seed=127)
+    rng = np.random.default_rng(128)
+    cache.words[1] = (rng.integers(low, high + 1, cache.words[1].shape) << 7) | rng.integers(0, 8, cache.words[1].shape) << 4 | 7
+    q = I4.bf16(rng.standard_normal((2, 2, 6, d)))
+    for tile in (64, 1024):
+        out, lse = _decode(cache, q, 2, tile=tile)
+        if low > 1:                                          # else out may be no normal number
+            _check_decode(cache, q, 2, out, lse, what=f"tile {tile}")
+        else:
+            for b, n in enumerate(cache.lens):
+                ref, ref_l, mass, _ = I4.attend(cache, b, q[b], n - 2 + np.arange(2))
+                assert np.all(np.abs(out[b] - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * mass[..., None] + 2.0 ** -134)
+                assert np.abs(lse[b] - ref_l).max() <= 1e-4
+
+
 def test_zero_v_rows_among_others():
     """An all-zero row is stored with the least scale there is."""
     cache = I4.Cache([400], Hkv=1, d=128, P=16, seed=107)
