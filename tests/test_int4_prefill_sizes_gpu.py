@@ -108,3 +108,13 @@ def test_prefill_takes_the_parts_that_its_workspace_has_room_for():
         out, lse = out.to(torch.float64).cpu().numpy(), lse.to(torch.float64).cpu().numpy()
         for at, t, ref in refs:
             I4.check(out[at:at + t], lse[at:at + t], ref, 2.0 ** -8, what=f"{n} bytes")
+
+
+@pytest.mark.parametrize("B", [511, 700])
+def test_prefill_of_a_chunk_among_hundreds_of_single_rows(B):
+    """Batches on both sides of the point from which every request has the same number of CTAs."""
+    lens, rows = _mixed(B, 155, 300, 40, 0.1)
+    cache = I4.Cache(lens, Hkv=1, d=128, P=16, seed=156)
+    q = I4.bf16(np.random.default_rng(157).standard_normal((sum(rows), 2, 128)))
+    out, lse = _prefill(cache, q, rows, uniform=False, pad=3)
+    _check_prefill(cache, q, rows, out, lse)
