@@ -150,7 +150,7 @@ SPLIT_TRAFFIC_CAPTURED = {
     },
 }
 # prefill_kernel on the full prefill workload (read, write): a few hundred MB on the device.
-PREFILL_TRAFFIC_CAPTURED = {"source_hash": "3447e365c41c00d8", "read": 109325568, "write": 85145600}
+PREFILL_TRAFFIC_CAPTURED = {"source_hash": "71962283b816bc95", "read": 108525568, "write": 84722944}
 
 
 def config_algorithmic_bytes(name: str, batch: int | None = None) -> int:

@@ -9,7 +9,7 @@
 //
 // Measured: 4 x 2048 rows, 32 query heads to 8 KV heads: 170 us, of which the expansion of 9 MB into 34 MB about 8; the rest
 // is the bf16 prefill kernel, bound by the chain of its two products and its softmax. 5 ragged chunks behind histories
-// of up to 7000 keys: 90 us (134 with their keys not split over CTAs).
+// of up to 7000 keys: 89 us (134 with their keys not split over CTAs).
 //
 // A NaN row of V (scale not finite) becomes a NaN row of K and zeros in V: a tensor-core product would carry a
 // NaN of V into rows that do not see the key (0 times NaN), while a NaN score is masked like any other.

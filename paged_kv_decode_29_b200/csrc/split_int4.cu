@@ -40,9 +40,9 @@
 //    (i, i + 4) are one f16 pair of V^T. So both operands come from the same 5 instructions per word.
 //
 // Measured (kernel times; 32 requests of 4096 tokens, 4 query heads to a KV head: 139 MB, 21.5 us at the copy rate):
-// 41 us with the combine. Bound by instruction issue and its latencies, not by DRAM: 270 instructions a warp and block,
-// half the issue slots and 47% of the ALU pipe busy at 16 warps a multiprocessor; the same kernel without its
-// copies takes 38.5 us, without its arithmetic 29. Other forms measured on the way, same case: a TMA producer warp with
+// 42.2 us with the combine. Bound by instruction issue and its latencies, not by DRAM: 290 instructions a warp and block,
+// half the issue slots and 48% of the ALU pipe busy at 16 warps a multiprocessor; an earlier form without its
+// copies took 38.5 us (41 with them), without its arithmetic 29. Other forms measured on the way, same case: a TMA producer warp with
 // two consumer warps that split the keys 57; four warps that split the head dims behind a TMA producer 48.5 (16-key
 // pages: the producer issues eight copies a block, each a loop over lanes); codes as E4M3 numbers for
 // mma.m16n8k32 62.9 (warp MMAs on E4M3 convert their operands to f16: the conversion pipe was 77% busy).
