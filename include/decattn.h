@@ -485,7 +485,7 @@ DECATTN_API int dec_attn_append_rope_int4(const dec_attn_shape *shape, const voi
 
 /* dec_attn_run over an INT4 cache: split + combine for shape->kv_dtype DECATTN_KV_INT4.
  *   kv_words  device uint16 [2][num_pages][Hkv][P], 16-byte aligned (codes too);
- *   out       bf16 [B][T][Hq][d], 16-byte aligned, rounded once from fp32; lse fp32 [B][T][Hq].
+ *   out       bf16 [B][T][Hq][d], 16-byte aligned, rounded once from fp32; it may be q itself; lse fp32 [B][T][Hq].
  * Other arguments, shapes, errors and stream rules as dec_attn_run; dense and block-sparse plans (this kernel has no
  * pipeline wait, so it never reports DECATTN_ETIMEOUT). Scores are fp32 sums of exact products of q and the
  * codes; a weight times a V scale is rounded to f16 for the second product: by at most 2^-11 of itself (bf16's rounding is

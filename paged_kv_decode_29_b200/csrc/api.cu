@@ -236,6 +236,9 @@ static int enqueue(int stages, const dec_attn_shape* shape, const void* q, const
     sp.k_codes = static_cast<const uint8_t*>(k_pages);
     sp.v_codes = static_cast<const uint8_t*>(v_pages);
     sp.kv_words = static_cast<const uint16_t*>(kv_words);
+    const int64_t q_bytes = (int64_t)s.batch * s.q_tokens * s.n_q_heads * D * 2;  // out has as many
+    const int64_t apart = static_cast<const char*>(q) - static_cast<const char*>(out);
+    sp.over_q = apart < q_bytes && -apart < q_bytes;
     sp.lse = lse;
     sp.part_o = part_o;
     sp.part_lse = part_lse;

@@ -52,6 +52,7 @@ struct SplitInt4Params : SplitParams {
   const uint8_t* v_codes;
   const uint16_t* kv_words; // row words [2][num_pages][Hkv][P]
   uint16_t* out_bf16;       // bf16 [B][T][Hq][D]
+  int over_q;               // out and q share memory
 };
 bool split_int4_supported(int D, int GT);                         // split_int4.cu
 cudaError_t launch_split_int4(const SplitInt4Params& p, int D, int device, cudaStream_t st);  // split_int4.cu

@@ -128,7 +128,8 @@ __device__ __forceinline__ bool bar_or(bool x) { return __syncthreads_or(x) != 0
 // differ. Without it such a tile is left wrong, and the return value asks the CTA for a second pass that has it. (One
 // pass for both is slower where no tile needs it, as the hot loop is out of registers: 32 requests of 4096 tokens 42.2 ->
 // 43.2 us, 16 query rows a KV head 105 -> 113. The second pass costs its CTAs the time once more, twice where every tile
-// is wide: 44 -> 91 -> 123.)
+// is wide: 44 -> 91 -> 123. Ending the first pass at its first wide tile, and starting the second one there, costs
+// the ordinary case 0.7 us.)
 template <int D, int NQ, bool WIDE>
 __device__ __forceinline__ bool i4_pass(const SplitInt4Params& p) {
   using C = I4Cfg<D, NQ>;
@@ -800,7 +801,9 @@ __device__ __noinline__ void i4_wide_pass(const SplitInt4Params& p) {
   i4_pass<D, NQ, true>(p);
 }
 
-template <int D, int NQ, int CPS>
+// OVER: out lies over q. The first pass writes out, so the second one goes alone. (A kernel of its own: the same as a
+// branch here costs the ordinary case 0.6 us.)
+template <int D, int NQ, int CPS, bool OVER>
 __global__ void __launch_bounds__(I4Cfg<D, NQ>::THREADS, CPS)
 split_int4_kernel(const __grid_constant__ SplitInt4Params p) {
   // Everything below reads or writes what earlier kernels of the stream may still be working on: the
@@ -811,7 +814,11 @@ split_int4_kernel(const __grid_constant__ SplitInt4Params p) {
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (int64_t)p.B * p.T * p.Hq;
        i += (int64_t)gridDim.x * blockDim.x)
     p.row_cnt[i] = 0;
-  if (i4_pass<D, NQ, false>(p)) i4_wide_pass<D, NQ>(p);
+  if constexpr (OVER) {
+    i4_pass<D, NQ, true>(p);
+  } else {
+    if (i4_pass<D, NQ, false>(p)) i4_wide_pass<D, NQ>(p);
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -819,7 +826,7 @@ template <int D, int NQ, int CPS>
 static cudaError_t launch_i4(const SplitInt4Params& p, int sms, cudaStream_t st) {
   using C = I4Cfg<D, NQ>;
   static_assert(CPS * (C::ALLOC + 1024) <= 228 * 1024, "the CTAs fit an SM's shared memory");
-  auto fn = split_int4_kernel<D, NQ, CPS>;
+  const auto fn = p.over_q ? split_int4_kernel<D, NQ, CPS, true> : split_int4_kernel<D, NQ, CPS, false>;
   if (!ensure_smem_attr((const void*)fn, C::ALLOC)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   const int groups = (p.GT + 8 * NQ - 1) / (8 * NQ);

@@ -336,3 +336,21 @@ def test_far_scales_bad_pages_and_nan_rows_together():
     cache.words[1, cache.table[1, 18], 0, 299 % 16] = 0x3F80
     want = _decode(cache, q, 3, tile=128)
     assert np.array_equal(out[1, :2], want[0][1, :2]) and np.array_equal(lse[1, :2], want[1][1, :2])
+
+
+@pytest.mark.parametrize("span", [0, 40])
+@pytest.mark.parametrize("tile", [64, 512])
+def test_out_over_q(tile, span):
+    """out may be q, also where a second pass reads q again."""
+    cache = I4.Cache([64, 40, 500, 0, 3], Hkv=2, d=128, P=16, seed=183)
+    if span:
+        _spread(cache, 184, span)
+    ref_q = I4.bf16(np.random.default_rng(185).standard_normal((5, 2, 24, 128)))
+    ref = _decode(cache, ref_q, 2, tile=tile)
+    _check_decode(cache, ref_q, 2, *ref)
+    dev, q = cache.to_device(), torch.from_numpy(ref_q).to(torch.bfloat16).cuda()
+    pl = da.plan(dev["lens"], 2, tile, max_total_kv_tokens=sum(cache.lens))
+    out, lse = da.run_int4(q, dev["k"], dev["v"], dev["words"], dev["tab"], dev["lens"], pl, out=q)
+    torch.cuda.synchronize()
+    assert out is q and np.array_equal(out.to(torch.float64).cpu().numpy(), ref[0])
+    assert np.array_equal(lse.to(torch.float64).cpu().numpy(), ref[1])
