@@ -513,7 +513,8 @@ DECATTN_API int64_t dec_attn_prefill_int4_packed_workspace_bytes(const dec_attn_
  * workspace) in place of the scales, and
  *   out  bf16 [rows][Hq][128], 16-byte aligned, rounded once from fp32; lse fp32 [rows][Hq].
  * Where the rows are few, the keys of a request are split over several CTAs and their fp32 parts merged (third
- * launch). Weights are rounded to bf16 for the second product, as dec_attn_prefill rounds them. A query row that
+ * launch). Weights are rounded to bf16 for the second product, as dec_attn_prefill rounds them; as there, scores times
+ * log2(e) have to stay below 2^30 and V below 2^120 over the number of keys in magnitude. A query row that
  * sees a NaN row of the cache gets NaN in out and lse; no other row does. Rows from cu_q_lens[batch] to
  * total_q_rows are left as they were. */
 DECATTN_API int dec_attn_prefill_int4(const dec_attn_shape *shape, const void *q, const void *k_pages,

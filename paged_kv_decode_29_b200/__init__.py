@@ -593,7 +593,7 @@ def run_int4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_w
              workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
              lse: torch.Tensor | None = None, stream=None):
     """dec_attn_run_int4: split + combine over an INT4 cache; returns (out bf16 [B][T][Hq][d], lse fp32
-    [B][T][Hq]). q: bf16 [B][T][Hq][d]; the cache as append_rope_int4 writes it; page_table, seq_lens, the
+    [B][T][Hq]). q: bf16 [B][T][Hq][d], which may be ``out``; the cache as append_rope_int4 writes it; page_table, seq_lens, the
     plan (dense or block-sparse) and the workspace as for ``run``, the workspace of a shape with KV_INT4."""
     lib = _lib or load_library()
     shape, _, dev = _int4_args(q, k_pages, v_pages, kv_words, page_table, seq_lens, None, workspace, out, lse)
